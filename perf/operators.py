@@ -475,7 +475,12 @@ def _plain_commit(case, s):
             to = s["tiles"][..., o:o + nb].unflatten(-1, (TILE, nb // TILE))
             of = s["draft"][..., o:o + nb].unflatten(-1, (TILE, nb // TILE))
         old = to[bi, :, pos // TILE, pos % TILE]               # [B, A, Hkv, bytes]
-        to[bi, :, pos // TILE, pos % TILE] = torch.where(keep, of[bi, :, 0, src], old)
+        row = of[bi, :, 0, src]
+        if name == "vcode" and case["vbits"] == 4:             # each slot keeps its 16-byte chunks in its own order
+            order = torch.arange(4, device="cuda") ^ (((pos % TILE // 2) ^ (src // 2)) & 3)[..., None]
+            row = row.unflatten(-1, (4, 16))
+            row = row.gather(3, order[:, :, None, :, None].expand(row.shape)).flatten(-2)
+        to[bi, :, pos // TILE, pos % TILE] = torch.where(keep, row, old)
     torch.add(s["lens"], s["accepted"], out=s["new_lens"])
     return [s["tiles"], s["new_lens"]]
 
