@@ -17,6 +17,8 @@ from .qjl import (  # noqa: F401
     QJLContext,
     QJLError,
     load_library,
+    qjl_cache_commit,
+    qjl_cache_read,
     qjl_ctx_guard,
     qjl_ctx_sketch,
     qjl_decode_attention,
@@ -28,5 +30,9 @@ from .qjl import (  # noqa: F401
     qjl_quantize_keys,
     qjl_quantize_keys_workspace_bytes,
     qjl_quantize_values,
+    qjl_rope,
+    qjl_rope_init,
     qjl_sketch_host,
+    qjl_tree_attention,
+    qjl_tree_attention_workspace_bytes,
 )

@@ -80,6 +80,24 @@ qjl_status check_input(const void* X, qjl_dtype dt, int T, int64_t sb, int64_t s
   return QJL_OK;
 }
 
+// The context's tables live on one device; a launch on another would read them
+// as foreign memory.
+qjl_status check_device(const qjl_ctx* ctx, const char* fn) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  if (dev != ctx->device) return fail(QJL_ERR_ARG, std::string(fn) + ": the context belongs to another device");
+  return QJL_OK;
+}
+
+// The context's wait limit in cycles at the maximum SM clock (a lower clock
+// only makes the wait longer in time).
+unsigned long long wait_cycles(const qjl_ctx* ctx) {
+  const unsigned long long c =
+      ctx->wait_ns * static_cast<unsigned long long>(ctx->clock_khz > 0 ? ctx->clock_khz : 2000000) / 1000000ull;
+  return c ? c : 1;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // CTAs of a decode launch: one per SM at most, and no more than the tiles
@@ -432,9 +450,7 @@ qjl_status decode_common(const char* fn, qjl_ctx* ctx, const qjl_cache* cache, c
   p.qblock_bytes = static_cast<int>(qjl::decode_qblock_bytes(g, ctx->m, ctx->m_out));
   p.part_o = reinterpret_cast<float*>(base + ws.part_o);
   p.part_ml = reinterpret_cast<float*>(base + ws.part_ml);
-  // limit in cycles at the maximum SM clock (a lower clock only makes the wait longer in time)
-  p.wait_cycles = ctx->wait_ns * static_cast<unsigned long long>(ctx->clock_khz > 0 ? ctx->clock_khz : 2000000) / 1000000ull;
-  if (p.wait_cycles == 0) p.wait_cycles = 1;
+  p.wait_cycles = wait_cycles(ctx);
   cudaError_t e = qjl::launch_decode(p, dtype, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return QJL_OK;
@@ -553,6 +569,228 @@ qjl_status qjl_exact_decode(qjl_kv_format format, const void* K, const void* V, 
                                            q_dtype == QJL_FP32, seqlens, scale * qjl::kLog2e, O,
                                            static_cast<float*>(workspace), s);
   if (e != cudaSuccess) return cuda_fail(e, "qjl_exact_decode");
+  return QJL_OK;
+}
+
+qjl_status qjl_rope_init(int rot_dim, double base, qjl_rope_layout layout, double factor, double original_len,
+                         double low, double high, double amplitude, qjl_rope_table* out) {
+  if (!out) return fail(QJL_ERR_ARG, "qjl_rope_init: null output pointer");
+  if (layout != QJL_ROPE_HALF && layout != QJL_ROPE_INTERLEAVED) return fail(QJL_ERR_ARG, "qjl_rope_init: layout");
+  if (rot_dim < 16 || rot_dim > qjl::kHeadDim || rot_dim % 16 != 0)
+    return fail(QJL_ERR_UNSUPPORTED, "qjl_rope_init: rot_dim must be a multiple of 16 in [16, 128]");
+  if (!(base > 0.0) || !std::isfinite(base) || !(factor > 0.0) || !std::isfinite(factor) || !std::isfinite(amplitude))
+    return fail(QJL_ERR_ARG, "qjl_rope_init: base and factor must be > 0 and finite, amplitude finite");
+  if (!(original_len >= 0.0) || !std::isfinite(original_len) ||
+      (original_len > 0.0 && !(low < high && std::isfinite(low) && std::isfinite(high))))
+    return fail(QJL_ERR_ARG, "qjl_rope_init: original_len must be >= 0, and low < high when it is positive");
+  qjl_rope_table t{};
+  t.rot_dim = rot_dim;
+  t.layout = layout;
+  t.amplitude = static_cast<float>(amplitude);
+  constexpr double kTwoPi = 6.283185307179586476925;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double turns = std::pow(base, -2.0 * i / rot_dim) / kTwoPi;
+    double s = 0.0;
+    if (original_len > 0.0) s = std::min(1.0, std::max(0.0, (original_len * turns - low) / (high - low)));
+    t.turns[i] = s * turns + (1.0 - s) * turns / factor;
+  }
+  *out = t;
+  return QJL_OK;
+}
+
+qjl_status qjl_rope(const qjl_rope_table* table, const qjl_rope_heads* heads, int n_heads, qjl_dtype dtype, int B,
+                    int T, const int32_t* positions, const int32_t* t_start, int inverse, void* stream) {
+  if (!table || !heads) return fail(QJL_ERR_ARG, "qjl_rope: null table or heads");
+  if (n_heads != 1 && n_heads != 2) return fail(QJL_ERR_ARG, "qjl_rope: n_heads must be 1 or 2");
+  if ((table->layout != QJL_ROPE_HALF && table->layout != QJL_ROPE_INTERLEAVED) || table->rot_dim < 16 ||
+      table->rot_dim > qjl::kHeadDim || table->rot_dim % 16 != 0)
+    return fail(QJL_ERR_ARG, "qjl_rope: the table was not filled by qjl_rope_init");
+  if (dtype != QJL_BF16 && dtype != QJL_FP32) return fail(QJL_ERR_ARG, "dtype must be QJL_BF16 or QJL_FP32");
+  if (B < 0 || T < 0) return fail(QJL_ERR_ARG, "qjl_rope: B and T must be >= 0");
+  qjl::RopeParams p{};
+  const int64_t q = dtype == QJL_BF16 ? 8 : 4;  // elements per 16 bytes
+  for (int k = 0; k < n_heads; ++k) {
+    const qjl_rope_heads& w = heads[k];
+    if (w.H < 1 || w.H > 65535) return fail(QJL_ERR_ARG, "qjl_rope: H must be in [1, 65535]");
+    const int64_t st[] = {w.x_sb, w.x_sh, w.x_st, w.y_sb, w.y_sh, w.y_st};
+    for (int64_t x : st)
+      if (x < 0 || x % q) return fail(QJL_ERR_ARG, "qjl_rope: strides must be non-negative multiples of 16 bytes");
+    if (w.x == w.y && (w.x_sb != w.y_sb || w.x_sh != w.y_sh || w.x_st != w.y_st))
+      return fail(QJL_ERR_ARG, "qjl_rope: in place, x and y must have the same strides");
+    if ((T > 1 && w.y_st < qjl::kHeadDim) || (w.H > 1 && w.y_sh < qjl::kHeadDim) || (B > 1 && w.y_sb < qjl::kHeadDim))
+      return fail(QJL_ERR_ARG, "qjl_rope: the rows of y must not overlap");
+    if (B > 0 && T > 0 && (!w.x || !w.y || !aligned16(w.x) || !aligned16(w.y)))
+      return fail(QJL_ERR_ARG, "qjl_rope: x and y must be non-null and 16-byte aligned");
+    p.heads[k] = w;
+  }
+  if (B == 0 || T == 0) return QJL_OK;
+  p.table = *table;
+  p.n_heads = n_heads;
+  p.B = B;
+  p.T = T;
+  p.positions = positions;
+  p.t_start = t_start;
+  p.inverse = inverse;
+  const cudaError_t e = qjl::launch_rope(p, dtype, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qjl_rope");
+  return QJL_OK;
+}
+
+qjl_status qjl_cache_read(qjl_ctx* ctx, const qjl_cache* cache, int T, const int32_t* t_start, const int32_t* seqlens,
+                          void* K_out, int64_t k_sb, int64_t k_sh, int64_t k_st, void* V_out, int64_t v_sb,
+                          int64_t v_sh, int64_t v_st, qjl_dtype dtype, void* stream) {
+  qjl_status st = check_cache(ctx, cache);
+  if (st == QJL_OK) st = check_device(ctx, "qjl_cache_read");
+  if (st != QJL_OK) return st;
+  if (!K_out && !V_out && T > 0) return fail(QJL_ERR_ARG, "qjl_cache_read: K_out and V_out are both null");
+  if (K_out) st = check_input(K_out, dtype, T, k_sb, k_sh, k_st, "K_out");
+  if (st == QJL_OK && V_out) st = check_input(V_out, dtype, T, v_sb, v_sh, v_st, "V_out");
+  if (st == QJL_OK && !K_out && !V_out) st = check_input(nullptr, dtype, T, 0, 0, qjl::kHeadDim, "K_out");
+  if (st != QJL_OK) return st;
+  if (T == 0) return QJL_OK;
+  if ((K_out && ((cache->B > 1 && k_sb < qjl::kHeadDim) || (cache->Hkv > 1 && k_sh < qjl::kHeadDim))) ||
+      (V_out && ((cache->B > 1 && v_sb < qjl::kHeadDim) || (cache->Hkv > 1 && v_sh < qjl::kHeadDim))))
+    return fail(QJL_ERR_ARG, "qjl_cache_read: the rows of an output must not overlap");
+  if (static_cast<int64_t>(cache->B) * cache->Hkv > 65535)
+    return fail(QJL_ERR_UNSUPPORTED, "B * Hkv must be at most 65535");
+  qjl::ReadParams p{};
+  p.tiles = static_cast<const unsigned char*>(cache->tiles);
+  p.tl = qjl::tile_layout(ctx->m, ctx->m_out, ctx->vbits);
+  p.B = cache->B;
+  p.Hkv = cache->Hkv;
+  p.cap = cache->cap;
+  p.T = T;
+  p.m = ctx->m;
+  p.m_out = ctx->m_out;
+  p.n_out = ctx->n_out;
+  p.t_start = t_start;
+  p.seqlens = seqlens;
+  p.S = ctx->S;
+  p.S_out = ctx->S_out;
+  p.idx = cache->outlier_idx;
+  p.K = K_out;
+  p.V = V_out;
+  p.k_sb = k_sb;
+  p.k_sh = k_sh;
+  p.k_st = k_st;
+  p.v_sb = v_sb;
+  p.v_sh = v_sh;
+  p.v_st = v_st;
+  p.num_sms = ctx->num_sms;
+  const cudaError_t e = qjl::launch_cache_read(p, dtype, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qjl_cache_read");
+  return QJL_OK;
+}
+
+size_t qjl_tree_attention_workspace_bytes(const qjl_ctx* ctx, int B, int N, int Hq, int Hkv) {
+  if (!ctx || B < 1 || N < 1 || N > qjl::kMaxDrafts || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
+  if (static_cast<int64_t>(B) * Hkv > 65535) return 0;
+  const int g = Hq / Hkv;
+  if (g != 1 && g != 2 && g != 4 && g != 8) return 0;
+  return qjl::tree_ws_bytes(B, N, Hq, Hkv, ctx->m, ctx->m_out, ctx->num_sms);
+}
+
+qjl_status qjl_tree_attention(qjl_ctx* ctx, const qjl_cache* cache, const qjl_cache* draft, const void* Q,
+                              int64_t q_sb, int64_t q_sn, int64_t q_sh, qjl_dtype dtype, int N, int Hq, int T,
+                              const int32_t* seqlens, const int32_t* n_draft, const uint64_t* tree_mask,
+                              float sm_scale, void* O, void* workspace, size_t workspace_bytes, void* stream) {
+  qjl_status st = check_cache(ctx, cache);
+  if (st == QJL_OK) st = check_cache(ctx, draft);
+  if (st == QJL_OK) st = check_device(ctx, "qjl_tree_attention");
+  if (st != QJL_OK) return st;
+  if (draft->B != cache->B || draft->Hkv != cache->Hkv)
+    return fail(QJL_ERR_ARG, "qjl_tree_attention: the draft cache must have the cache's B and Hkv");
+  if (N < 1 || N > qjl::kMaxDrafts || N > draft->cap)
+    return fail(QJL_ERR_ARG, "qjl_tree_attention: N must be in [1, 64] and at most the draft cache's cap");
+  if (dtype != QJL_BF16 && dtype != QJL_FP32) return fail(QJL_ERR_ARG, "dtype must be QJL_BF16 or QJL_FP32");
+  if (Hq < 1 || Hq % cache->Hkv != 0) return fail(QJL_ERR_ARG, "Hq must be a positive multiple of Hkv");
+  const int g = Hq / cache->Hkv;
+  if (g != 1 && g != 2 && g != 4 && g != 8) return fail(QJL_ERR_UNSUPPORTED, "Hq / Hkv must be 1, 2, 4 or 8");
+  if (static_cast<int64_t>(cache->B) * cache->Hkv > 65535)
+    return fail(QJL_ERR_UNSUPPORTED, "B * Hkv must be at most 65535");
+  if (T < 0 || T > cache->cap) return fail(QJL_ERR_ARG, "T must be in [0, cap]");
+  if (!Q || !O || !aligned16(Q) || !aligned16(O)) return fail(QJL_ERR_ARG, "Q and O must be 16-byte aligned");
+  const int64_t q = dtype == QJL_BF16 ? 8 : 4;  // elements per 16 bytes
+  if (q_sb < 0 || q_sn < 0 || q_sh < 0 || q_sb % q || q_sn % q || q_sh % q)
+    return fail(QJL_ERR_ARG, "qjl_tree_attention: Q strides must be non-negative multiples of 16 bytes");
+  if (tree_mask && (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+    return fail(QJL_ERR_ARG, "qjl_tree_attention: tree_mask must be 8-byte aligned");
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < qjl_tree_attention_workspace_bytes(ctx, cache->B, N, Hq, cache->Hkv))
+    return fail(QJL_ERR_WORKSPACE, "qjl_tree_attention: workspace missing, misaligned or too small");
+  qjl::TreeParams p{};
+  p.tiles = static_cast<const unsigned char*>(cache->tiles);
+  p.draft = static_cast<const unsigned char*>(draft->tiles);
+  p.tl = qjl::tile_layout(ctx->m, ctx->m_out, ctx->vbits);
+  p.B = cache->B;
+  p.Hq = Hq;
+  p.Hkv = cache->Hkv;
+  p.cap = cache->cap;
+  p.draft_cap = draft->cap;
+  p.N = N;
+  p.T = T;
+  p.G = g;
+  p.m = ctx->m;
+  p.m_out = ctx->m_out;
+  p.n_out = ctx->n_out;
+  p.Q = Q;
+  p.q_sb = q_sb;
+  p.q_sn = q_sn;
+  p.q_sh = q_sh;
+  p.seqlens = seqlens;
+  p.n_draft = n_draft;
+  p.mask = tree_mask;
+  p.S = ctx->S;
+  p.St = ctx->St;
+  p.S_out = ctx->S_out;
+  p.S_frag = reinterpret_cast<const uint4*>(ctx->S_frag);
+  p.idx = cache->outlier_idx;
+  const float scale = sm_scale > 0.0f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(ctx->d));
+  p.sm_scale_log2 = scale * qjl::kLog2e;
+  p.O = O;
+  p.ws = static_cast<unsigned char*>(workspace);
+  p.num_sms = ctx->num_sms;
+  p.wait_cycles = wait_cycles(ctx);
+  const cudaError_t e = qjl::launch_tree_attention(p, dtype, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qjl_tree_attention");
+  return QJL_OK;
+}
+
+qjl_status qjl_cache_commit(qjl_ctx* ctx, const qjl_cache* cache, const qjl_cache* draft, int A, const int32_t* path,
+                            const int32_t* n_accepted, const int32_t* seqlens, int32_t* seqlens_out, void* stream) {
+  qjl_status st = check_cache(ctx, cache);
+  if (st == QJL_OK) st = check_cache(ctx, draft);
+  if (st == QJL_OK) st = check_device(ctx, "qjl_cache_commit");
+  if (st != QJL_OK) return st;
+  if (draft->B != cache->B || draft->Hkv != cache->Hkv)
+    return fail(QJL_ERR_ARG, "qjl_cache_commit: the draft cache must have the cache's B and Hkv");
+  if (draft->tiles == cache->tiles) return fail(QJL_ERR_ARG, "qjl_cache_commit: the two caches share their tiles");
+  if (A < 0 || A > 65535 * 8) return fail(QJL_ERR_ARG, "qjl_cache_commit: A must be in [0, 524280]");
+  if ((A > 0 && !path) || !n_accepted || !seqlens)
+    return fail(QJL_ERR_ARG, "qjl_cache_commit: null path, n_accepted or seqlens");
+  if (seqlens_out) {
+    const int32_t *a = seqlens, *o = seqlens_out;
+    if (a < o + cache->B && o < a + cache->B)
+      return fail(QJL_ERR_ARG, "qjl_cache_commit: seqlens_out overlaps seqlens");
+  }
+  if (cache->B > 65535) return fail(QJL_ERR_UNSUPPORTED, "B must be at most 65535");
+  qjl::CommitParams p{};
+  p.tiles = static_cast<unsigned char*>(cache->tiles);
+  p.draft = static_cast<const unsigned char*>(draft->tiles);
+  p.tl = qjl::tile_layout(ctx->m, ctx->m_out, ctx->vbits);
+  p.B = cache->B;
+  p.Hkv = cache->Hkv;
+  p.cap = cache->cap;
+  p.draft_cap = draft->cap;
+  p.A = A;
+  p.m = ctx->m;
+  p.m_out = ctx->m_out;
+  p.path = path;
+  p.n_accepted = n_accepted;
+  p.seqlens = seqlens;
+  p.seqlens_out = seqlens_out;
+  const cudaError_t e = qjl::launch_cache_commit(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qjl_cache_commit");
   return QJL_OK;
 }
 

@@ -283,6 +283,55 @@ inline DecodeWsLayout decode_ws_layout(int B, int Hq, int Hkv, int num_sms, int 
   return w;
 }
 
+struct RopeParams {
+  qjl_rope_table table;
+  qjl_rope_heads heads[2];
+  int n_heads, B, T;
+  const int32_t* positions;  // [B, T] or null
+  const int32_t* t_start;    // [B] or null (used when positions is null)
+  int inverse;
+};
+
+struct ReadParams {
+  const unsigned char* tiles;
+  TileLayout tl;
+  int B, Hkv, cap, T, m, m_out, n_out;
+  const int32_t *t_start, *seqlens;
+  const __nv_bfloat16 *S, *S_out;  // [m, d], [m_out, d]
+  const int32_t* idx;              // [B, Hkv, n_out]
+  void *K, *V;                     // outputs, either may be null
+  int64_t k_sb, k_sh, k_st, v_sb, v_sh, v_st;
+  int num_sms;
+};
+
+struct CommitParams {
+  unsigned char* tiles;
+  const unsigned char* draft;
+  TileLayout tl;
+  int B, Hkv, cap, draft_cap, A, m, m_out;
+  const int32_t *path, *n_accepted, *seqlens;
+  int32_t* seqlens_out;
+};
+
+struct TreeParams {
+  const unsigned char *tiles, *draft;
+  TileLayout tl;
+  int B, Hq, Hkv, cap, draft_cap, N, T, G, m, m_out, n_out;
+  const void* Q;
+  int64_t q_sb, q_sn, q_sh;
+  const int32_t *seqlens, *n_draft;
+  const uint64_t* mask;
+  const __nv_bfloat16 *S, *St, *S_out;
+  const uint4* S_frag;
+  const int32_t* idx;
+  float sm_scale_log2;
+  void* O;
+  unsigned char* ws;
+  int num_sms;
+  unsigned long long wait_cycles;
+};
+constexpr int kMaxDrafts = 64;  // bits of a tree mask row
+
 // Launchers (return the cudaGetLastError() of the launches).
 cudaError_t launch_quantize_values(const ValuesParams& p, qjl_dtype dt, cudaStream_t s);
 int64_t exact_decode_chunks(int cap);
@@ -302,6 +351,11 @@ cudaError_t launch_sketch_keys(const KeysParams& p, qjl_dtype dt, cudaStream_t s
 bool sketch_keys_tc_applies(const KeysParams& p, qjl_dtype dt);
 cudaError_t launch_sketch_keys_tc(const KeysParams& p, int num_sms, cudaStream_t s);
 void tc_fill_s_image(const uint16_t* S, int rows, uint16_t* img);  // host: [rows, d] -> image [rows * d]
+cudaError_t launch_rope(const RopeParams& p, qjl_dtype dt, cudaStream_t s);
+cudaError_t launch_cache_read(const ReadParams& p, qjl_dtype dt, cudaStream_t s);
+cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t s);
+size_t tree_ws_bytes(int B, int N, int Hq, int Hkv, int m, int m_out, int num_sms);
+cudaError_t launch_tree_attention(const TreeParams& p, qjl_dtype dt, cudaStream_t s);
 cudaError_t launch_decode(const DecodeParams& p, qjl_dtype dt, cudaStream_t s);
 // host: S [m, d] and S_out [m_out, d] (bf16 bits) -> S_frag [(m + m_out) * d] (decode.cu)
 void decode_fill_s_frag(const uint16_t* S, const uint16_t* S_out, int m, int m_out, uint16_t* out);

@@ -35,7 +35,11 @@ EXPORTED = [
     "qjl_decode_workspace_status", "qjl_decode_attention_static", "qjl_decode_attention_partial",
     "qjl_merge_partials", "qjl_fp8_quantize", "qjl_exact_decode_workspace_bytes", "qjl_exact_decode",
     "qjl_minmax_quantize",
+    "qjl_rope_init", "qjl_rope", "qjl_cache_read", "qjl_tree_attention_workspace_bytes", "qjl_tree_attention",
+    "qjl_cache_commit",
 ]
+QJL_ROPE_HALF, QJL_ROPE_INTERLEAVED = 0, 1
+MAX_DRAFTS = 64  # drafted tokens of a sequence at most
 QJL_KV_BF16, QJL_KV_FP8_E4M3, QJL_KV_MINMAX2, QJL_KV_MINMAX4 = 0, 1, 2, 3
 _ROW_FORMAT = {128: QJL_KV_FP8_E4M3, 48: QJL_KV_MINMAX2, 80: QJL_KV_MINMAX4}  # uint8 row bytes -> format
 
@@ -60,6 +64,21 @@ class qjl_cache(ctypes.Structure):
     ]
 
 
+class qjl_rope_table(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("amplitude", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("turns", ctypes.c_double * 64),
+    ]
+
+
+class qjl_rope_heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int32)] + [
+        (n, ctypes.c_int64) for n in ("x_sb", "x_sh", "x_st", "y_sb", "y_sh", "y_st")]
+
+
 _lib = None
 
 
@@ -73,6 +92,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                            "`python -m decode_attention_qjl_b200.build` (there is no fallback path)")
     L = ctypes.CDLL(path)
     vp, i32, i64, u64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
+    f64 = ctypes.c_double
     cachep = ctypes.POINTER(qjl_cache)
     sig = {
         "qjl_init": (i32, [u64, i32, i32, i32, i32, ctypes.POINTER(vp)]),
@@ -102,6 +122,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "qjl_minmax_quantize": (i32, [vp, i32, i64, i32, vp, vp]),
         "qjl_exact_decode": (i32, [i32, vp, vp, ctypes.c_float, ctypes.c_float, i32, i32, i32, i32, i32, vp, i32, vp,
                                    ctypes.c_float, vp, vp, sz, vp]),
+        "qjl_rope_init": (i32, [i32, f64, i32, f64, f64, f64, f64, f64, ctypes.POINTER(qjl_rope_table)]),
+        "qjl_rope": (i32, [ctypes.POINTER(qjl_rope_table), ctypes.POINTER(qjl_rope_heads), i32, i32, i32, i32, vp, vp,
+                           i32, vp]),
+        "qjl_cache_read": (i32, [vp, cachep, i32, vp, vp, vp, i64, i64, i64, vp, i64, i64, i64, i32, vp]),
+        "qjl_tree_attention_workspace_bytes": (sz, [vp, i32, i32, i32, i32]),
+        "qjl_tree_attention": (i32, [vp, cachep, cachep, vp, i64, i64, i64, i32, i32, i32, i32, vp, vp, vp,
+                                     ctypes.c_float, vp, vp, sz, vp]),
+        "qjl_cache_commit": (i32, [vp, cachep, cachep, i32, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -232,6 +260,15 @@ class QJLCache:
             tiles=torch.zeros(B, Hkv, cap // TILE_TOKENS, tb, dtype=torch.uint8, device=device),
             B=B, Hkv=Hkv, cap=cap, m=m, m_out=m_out, value_bits=value_bits,
         )
+
+    def draft(self, slots: int = MAX_DRAFTS):
+        """Zero-filled draft cache for this one: the same heads and outlier channels, `slots` tokens."""
+        import torch
+
+        nt = -(-max(slots, 1) // TILE_TOKENS)
+        tiles = torch.zeros(self.B, self.Hkv, nt, self.tiles.shape[-1], dtype=torch.uint8, device=self.tiles.device)
+        return QJLCache(self.outlier_idx, tiles, self.B, self.Hkv, nt * TILE_TOKENS, self.m, self.m_out,
+                        self.value_bits)
 
     def struct(self) -> qjl_cache:
         return qjl_cache(self.outlier_idx.data_ptr(), self.tiles.data_ptr(), self.B, self.Hkv, self.cap)
@@ -410,6 +447,141 @@ def qjl_exact_decode(K, V, Q, O, T: int | None = None, seqlens=None, sm_scale: f
     return O
 
 
+def _device_tensors(fn: str, *tensors):
+    """The tensors must lie on the current CUDA device, where the call runs."""
+    import torch
+
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (t.device.type != "cuda" or t.device.index != cur):
+            raise ValueError(f"{fn}: tensor on {t.device}, the call runs on cuda:{cur}")
+
+
+def _index_tensor(fn: str, name: str, t, shape, dtype):
+    """An optional index argument: contiguous, of the given shape and dtype."""
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _head_rows(fn: str, name: str, t, shape, dtype):
+    """A tensor of head rows: the given shape and dtype, last dim contiguous."""
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.stride(-1) != 1):
+        raise ValueError(f"{fn}: {name} must be {dtype} {tuple(shape)} with a contiguous last dim, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def qjl_rope_init(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0,
+                  original_len: float = 0.0, low: float = 1.0, high: float = 4.0,
+                  amplitude: float = 1.0) -> qjl_rope_table:
+    """Rotation frequencies for qjl_rope; host only. `factor` divides all of them, or, with `original_len`,
+    those of planes that turn less than `low` times within it (none of those above `high`, a ramp between)."""
+    table = qjl_rope_table()
+    _check("qjl_rope_init", load_library().qjl_rope_init(rot_dim, base, QJL_ROPE_INTERLEAVED if interleaved
+                                                         else QJL_ROPE_HALF, factor, original_len, low, high,
+                                                         amplitude, ctypes.byref(table)))
+    return table
+
+
+def qjl_rope(table: qjl_rope_table, Q, K=None, positions=None, t_start=None, Q_out=None, K_out=None,
+             inverse: bool = False, stream=None):
+    """Rotary positions of Q [B, Hq, T, d] and, in the same launch, K [B, Hkv, T, d] (device, bf16 or fp32, last dim
+    contiguous; any strides of whole 16-byte units, e.g. a transposed [B, T, H, d]). positions: int32 [B, T], or
+    t_start: int32 [B] (position t_start[b] + t), or neither (position t). Q_out / K_out may be Q / K themselves.
+    inverse: rotate back, which is also the gradient. Returns Q_out, or (Q_out, K_out) when K is given."""
+    import torch
+
+    pairs = [(Q, Q_out)] + ([(K, K_out)] if K is not None else [])
+    B, _, T, d = Q.shape
+    arr = (qjl_rope_heads * 2)()
+    outs = []
+    for n, (x, y) in enumerate(pairs):
+        if x.dim() != 4 or x.shape[0] != B or x.shape[2] != T or x.shape[3] != HEAD_DIM:
+            raise ValueError(f"qjl_rope: tensors must be [B, H, T, {HEAD_DIM}] with one B and T")
+        y = torch.empty_like(x) if y is None else y
+        _head_rows("qjl_rope", "an input", x, x.shape, Q.dtype)
+        _head_rows("qjl_rope", "an output", y, x.shape, Q.dtype)
+        arr[n] = qjl_rope_heads(x.data_ptr(), y.data_ptr(), x.shape[1], *x.stride()[:3], *y.stride()[:3])
+        outs.append(y)
+    _index_tensor("qjl_rope", "positions", positions, (B, T), torch.int32)
+    _index_tensor("qjl_rope", "t_start", t_start, (B,), torch.int32)
+    _device_tensors("qjl_rope", Q, K, positions, t_start, *outs)
+    _check("qjl_rope", load_library().qjl_rope(ctypes.byref(table), arr, len(pairs), _dtype_code(Q), B, T,
+                                               _ptr(positions), _ptr(t_start), int(inverse), _stream(stream)))
+    return outs[0] if K is None else tuple(outs)
+
+
+def qjl_cache_read(ctx, cache: QJLCache, T: int, K_out=None, V_out=None, t_start=None, seqlens=None, stream=None):
+    """Dense keys and values [B, Hkv, T, d] of the cached tokens at positions t_start[b] + t (0 + t) below
+    seqlens[b] (the capacity); other rows stay as they were. K_out, V_out: device bf16 or fp32 (one dtype)."""
+    import torch
+
+    out = K_out if K_out is not None else V_out
+    if out is None:
+        raise ValueError("qjl_cache_read: K_out and V_out are both missing")
+    strides = []
+    for name, t in (("K_out", K_out), ("V_out", V_out)):
+        _head_rows("qjl_cache_read", name, t, (cache.B, cache.Hkv, T, HEAD_DIM), out.dtype)
+        strides.append((0, 0, 0) if t is None else t.stride()[:3])
+    _index_tensor("qjl_cache_read", "t_start", t_start, (cache.B,), torch.int32)
+    _index_tensor("qjl_cache_read", "seqlens", seqlens, (cache.B,), torch.int32)
+    _device_tensors("qjl_cache_read", K_out, V_out, t_start, seqlens, cache.tiles)
+    st = load_library().qjl_cache_read(ctx, ctypes.byref(cache.struct()), T, _ptr(t_start), _ptr(seqlens), _ptr(K_out),
+                                       *strides[0], _ptr(V_out), *strides[1], _dtype_code(out), _stream(stream))
+    _check("qjl_cache_read", st)
+    return K_out, V_out
+
+
+def qjl_tree_attention_workspace_bytes(ctx, B: int, N: int, Hq: int, Hkv: int) -> int:
+    return int(load_library().qjl_tree_attention_workspace_bytes(ctx, B, N, Hq, Hkv))
+
+
+def qjl_tree_attention(ctx, cache: QJLCache, draft: QJLCache, Q, T: int, O, seqlens=None, n_draft=None, tree_mask=None,
+                       sm_scale: float = 0.0, workspace=None, stream=None):
+    """Attention of drafted tokens Q (device [B, N, Hq, d], bf16 or fp32, last dim contiguous) over the committed
+    cache (T tokens, or seqlens[b]) and the draft cache (QJLCache.draft). tree_mask: int64 [B, N], bit j of row i
+    set when drafted token i attends to drafted token j (None: j <= i). n_draft: int32 [B], drafted tokens of each
+    sequence (None: N). O: device [B, N, Hq, d] of Q's dtype, contiguous, written."""
+    import torch
+
+    B, N, Hq, d = Q.shape
+    if B != cache.B or d != HEAD_DIM:
+        raise ValueError(f"qjl_tree_attention: Q must be [{cache.B}, N, Hq, {HEAD_DIM}]")
+    _head_rows("qjl_tree_attention", "Q", Q, Q.shape, Q.dtype)
+    _head_rows("qjl_tree_attention", "O", O, Q.shape, Q.dtype)
+    if not O.is_contiguous():
+        raise ValueError("qjl_tree_attention: O must be contiguous")
+    _index_tensor("qjl_tree_attention", "seqlens", seqlens, (B,), torch.int32)
+    _index_tensor("qjl_tree_attention", "n_draft", n_draft, (B,), torch.int32)
+    _index_tensor("qjl_tree_attention", "tree_mask", tree_mask, (B, N), torch.int64)
+    _device_tensors("qjl_tree_attention", Q, O, seqlens, n_draft, tree_mask, workspace, cache.tiles, draft.tiles)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = load_library().qjl_tree_attention(ctx, ctypes.byref(cache.struct()), ctypes.byref(draft.struct()), _ptr(Q),
+                                           *Q.stride()[:3], _dtype_code(Q), N, Hq, T, _ptr(seqlens), _ptr(n_draft),
+                                           _ptr(tree_mask), sm_scale, _ptr(O), _ptr(workspace), ws_bytes,
+                                           _stream(stream))
+    _check("qjl_tree_attention", st)
+    return O
+
+
+def qjl_cache_commit(ctx, cache: QJLCache, draft: QJLCache, path, n_accepted, seqlens, seqlens_out=None, stream=None):
+    """Copy draft slots path[b, j], j < n_accepted[b], to cache slots seqlens[b] + j; path: device int32 [B, A],
+    the others int32 [B]. seqlens_out (not seqlens itself) receives the new lengths."""
+    import torch
+
+    _index_tensor("qjl_cache_commit", "path", path, (cache.B, path.shape[-1]), torch.int32)
+    for name, t in (("n_accepted", n_accepted), ("seqlens", seqlens), ("seqlens_out", seqlens_out)):
+        _index_tensor("qjl_cache_commit", name, t, (cache.B,), torch.int32)
+    _device_tensors("qjl_cache_commit", path, n_accepted, seqlens, seqlens_out, cache.tiles, draft.tiles)
+    st = load_library().qjl_cache_commit(ctx, ctypes.byref(cache.struct()), ctypes.byref(draft.struct()),
+                                         path.shape[1], _ptr(path), _ptr(n_accepted), _ptr(seqlens),
+                                         _ptr(seqlens_out), _stream(stream))
+    _check("qjl_cache_commit", st)
+    return seqlens_out
+
+
 def qjl_set_wait_limit(ctx, ns: int) -> None:
     _check("qjl_set_wait_limit", load_library().qjl_set_wait_limit(ctx, int(ns)))
 
@@ -464,6 +636,12 @@ class QJLContext:
 
         n = qjl_decode_workspace_bytes(self.handle, B, Hq, Hkv, T)
         return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+
+    def tree_workspace(self, B: int, N: int, Hq: int, Hkv: int, device="cuda"):
+        import torch
+
+        n = qjl_tree_attention_workspace_bytes(self.handle, B, N, Hq, Hkv)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
     def keys_workspace(self, B: int, Hkv: int, device="cuda"):
         import torch

@@ -325,6 +325,158 @@ qjl_status qjl_decode_workspace_status(const qjl_ctx* ctx, void* workspace, int 
 
 /*
  * ---------------------------------------------------------------------------
+ * A speculative decode step over the QJL cache: the drafted tokens' queries and
+ * keys are rotated (qjl_rope), the drafts are sketched into a draft cache
+ * (qjl_quantize_keys with QJL_APPEND and qjl_quantize_values, token t in slot
+ * t), every drafted token attends to the committed cache and to its ancestors
+ * among the drafts (qjl_tree_attention), and the accepted drafts are copied
+ * into the cache (qjl_cache_commit). qjl_cache_read gives cached tokens back as
+ * dense keys and values. The pages have no counterpart: they describe decoding
+ * one token at a time.
+ *
+ * A draft cache is a qjl_cache of the same context, B and Hkv whose
+ * outlier_idx is the committed cache's, so that its keys are sketched with the
+ * channels chosen at prefill; slot i of (b, kv head) holds drafted token i of
+ * sequence b. cap = 64 is enough (at most 64 drafts).
+ *
+ * These entry points run on the device of the context, which must be the
+ * current one (else QJL_ERR_ARG); qjl_rope runs on the current device.
+ * ---------------------------------------------------------------------------
+ */
+typedef enum {
+  QJL_ROPE_HALF = 0,       /* plane i turns dims (i, i + rot_dim / 2) */
+  QJL_ROPE_INTERLEAVED = 1 /* plane i turns dims (2i, 2i + 1) */
+} qjl_rope_layout;
+
+/* Filled by qjl_rope_init; plain data, owned by the caller, reusable by any number of calls. */
+typedef struct {
+  int32_t rot_dim;
+  int32_t layout;    /* a qjl_rope_layout */
+  float amplitude;
+  int32_t reserved;
+  double turns[64];  /* turns per position of plane i: f_i / (2 pi) */
+} qjl_rope_table;
+
+/* One tensor of a qjl_rope call: element (b, h, t, c) at x[b*x_sb + h*x_sh + t*x_st + c], likewise y. */
+typedef struct {
+  const void* x;
+  void* y;        /* may equal x (with x's strides); otherwise x and y must not overlap */
+  int32_t H;      /* heads */
+  int64_t x_sb, x_sh, x_st; /* element strides, multiples of 16 bytes, >= 0 */
+  int64_t y_sb, y_sh, y_st;
+} qjl_rope_heads;
+
+/*
+ * qjl_rope_init - the rotation frequencies of rotary positions.
+ *   Computes, for plane i < rot_dim / 2, f_i = base^(-2i / rot_dim), then
+ *     original_len == 0: f_i / factor;
+ *     original_len > 0:  with r = original_len f_i / (2 pi) the turns within the
+ *       original length and s = clamp((r - low) / (high - low), 0, 1):
+ *       s f_i + (1 - s) f_i / factor
+ *       (wavelengths stretched by parts: those far shorter than the original
+ *       length stay, those far longer are divided by factor).
+ *   factor = 1 with original_len = 0 is the plain rotation.
+ *   rot_dim: a multiple of 16 in [16, 128]; dims rot_dim.. of a head are copied.
+ *   base > 0, factor > 0, amplitude finite (multiplies the rotated dims),
+ *   original_len >= 0, low < high when original_len > 0.
+ *   Host only, needs no GPU. Errors: QJL_ERR_ARG, QJL_ERR_UNSUPPORTED (rot_dim).
+ */
+qjl_status qjl_rope_init(int rot_dim, double base, qjl_rope_layout layout, double factor, double original_len,
+                         double low, double high, double amplitude, qjl_rope_table* out);
+
+/*
+ * qjl_rope - rotary positions of one or two tensors (a step's queries and keys).
+ *   Computes, for token t of sequence b at position P and plane i with dims
+ *   (u, v), a = P f_i:
+ *     y_u = amplitude (x_u cos a - x_v sin a),
+ *     y_v = amplitude (x_v cos a + x_u sin a);   inverse != 0: a -> -a,
+ *   which is the gradient with respect to x of the forward rotation, and with
+ *   amplitude 1 its inverse. Angles are reduced in fp64, so far positions lose
+ *   nothing; sin, cos and the products are fp32, rounded once to the dtype.
+ *   heads: n_heads (1 or 2) tensors [B, H, T, d] (d = 128) of the same dtype,
+ *   16-byte aligned.
+ *   positions: device int32 [B, T], or NULL: P = (t_start ? t_start[b] : 0) + t.
+ *   Errors: QJL_ERR_ARG, QJL_ERR_CUDA. B * T == 0 enqueues nothing.
+ */
+qjl_status qjl_rope(const qjl_rope_table* table, const qjl_rope_heads* heads, int n_heads, qjl_dtype dtype, int B,
+                    int T, const int32_t* positions, const int32_t* t_start, int inverse, void* stream);
+
+/*
+ * qjl_cache_read - the dense keys and values that cached tokens stand for.
+ *   Computes for token t < T of sequence b, at position P = (t_start ?
+ *   t_start[b] : 0) + t:
+ *     K_hat_c = sqrt(pi/2)/m |k_in| sum_i sign_i S_ic          (inlier channel c)
+ *             = sqrt(pi/2)/m_out |k_out| sum_i sign_out_i S_out_ic  (outlier channel)
+ *     V_hat_c = zero + code * scale,
+ *   so that <q, K_hat> is the estimator's score of any query q (file comment).
+ *   Positions outside [0, min(seqlens[b], cap)) (seqlens NULL: [0, cap)) leave
+ *   their rows of K_out and V_out as they were.
+ *   K_out, V_out: device, dtype `dtype`, element (b, h, t, c) at
+ *   K_out[b*k_sb + h*k_sh + t*k_st + c], likewise V_out; 16-byte aligned, strides
+ *   as K in qjl_quantize_keys and rows that do not overlap; either may be NULL.
+ *   Errors: QJL_ERR_ARG, QJL_ERR_CUDA. T == 0 enqueues nothing.
+ */
+qjl_status qjl_cache_read(qjl_ctx* ctx, const qjl_cache* cache, int T, const int32_t* t_start, const int32_t* seqlens,
+                          void* K_out, int64_t k_sb, int64_t k_sh, int64_t k_st, void* V_out, int64_t v_sb,
+                          int64_t v_sh, int64_t v_st, qjl_dtype dtype, void* stream);
+
+/*
+ * qjl_tree_attention_workspace_bytes - device workspace of qjl_tree_attention
+ * for B sequences of up to N drafted tokens; 0 for an invalid shape.
+ */
+size_t qjl_tree_attention_workspace_bytes(const qjl_ctx* ctx, int B, int N, int Hq, int Hkv);
+
+/*
+ * qjl_tree_attention - attention of drafted tokens over the QJL cache.
+ *   Computes for every sequence b, drafted token i < n_draft[b] and query head
+ *   h (kv head h / (Hq/Hkv)), with the estimator's scores of qjl_decode_attention:
+ *     O[b,i,h] = softmax(sm_scale * score) over the committed tokens t < len_b
+ *                and the drafted tokens j < n_draft[b] with bit j of
+ *                tree_mask[b,i] set, times their values.
+ *   What bit i (the token itself) holds is the caller's choice; a token whose
+ *   row leaves nothing gives 0, and so do the rows i >= n_draft[b].
+ *   cache: the committed tokens; T, seqlens as in qjl_decode_attention.
+ *   draft: the draft cache (above), cap >= N.
+ *   Q: device, dtype `dtype`, element (b, i, h, c) at Q[b*q_sb + i*q_sn + h*q_sh
+ *      + c] (element strides, multiples of 16 bytes, >= 0; 16-byte aligned).
+ *   N: 1 .. 64. n_draft: device int32 [B], clamped to [0, N], or NULL (= N).
+ *   tree_mask: device uint64 [B, N], or NULL: a chain (token i attends to j <= i).
+ *   O: device [B, N, Hq, d] of the dtype of Q, contiguous, written.
+ *   Precision: fp32 queries take fp32 products throughout. bf16 queries take the
+ *      tensor cores: the projected query in fp16 (scaled by a power of two per
+ *      row, so 11 significant bits at its largest entry), softmax weights and
+ *      dequantised values in fp16, all sums in fp32; each adds about 2^-12 of
+ *      the row's values, an eighth of the output's own bf16 rounding.
+ *   workspace: device, qjl_tree_attention_workspace_bytes bytes, 16-byte
+ *      aligned, no initial contents needed. Calls that share one must not
+ *      overlap on the GPU.
+ *   Every wait inside is bounded by qjl_set_wait_limit; when one runs out, the
+ *   rows it belongs to become NaN.
+ *   Errors: QJL_ERR_ARG, QJL_ERR_UNSUPPORTED (Hq / Hkv not 1, 2, 4 or 8),
+ *   QJL_ERR_WORKSPACE, QJL_ERR_CUDA.
+ */
+qjl_status qjl_tree_attention(qjl_ctx* ctx, const qjl_cache* cache, const qjl_cache* draft, const void* Q,
+                              int64_t q_sb, int64_t q_sn, int64_t q_sh, qjl_dtype dtype, int N, int Hq, int T,
+                              const int32_t* seqlens, const int32_t* n_draft, const uint64_t* tree_mask,
+                              float sm_scale, void* O, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * qjl_cache_commit - copy accepted drafted tokens into the cache.
+ *   For j < n_accepted[b] (clamped to [0, A]) slot path[b, j] of the draft cache
+ *   is copied, in every section and for every kv head, to slot len_b + j of the
+ *   cache, with len_b = seqlens[b] clamped to [0, cap]. A path entry outside
+ *   the draft cache or a target slot >= cap is skipped. seqlens_out[b] =
+ *   min(len_b + n_accepted[b], cap).
+ *   path: device int32 [B, A]; n_accepted, seqlens, seqlens_out: device int32
+ *   [B]; seqlens_out must not overlap seqlens, and may be NULL. The two caches
+ *   must not share tiles.
+ *   Errors: QJL_ERR_ARG, QJL_ERR_CUDA. A == 0 only writes seqlens_out.
+ */
+qjl_status qjl_cache_commit(qjl_ctx* ctx, const qjl_cache* cache, const qjl_cache* draft, int A, const int32_t* path,
+                            const int32_t* n_accepted, const int32_t* seqlens, int32_t* seqlens_out, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Comparison kernels: decode over an unquantised bf16 cache and over an FP8
  * cache, on the same shapes as the QJL path ("2 numbers out of 128 destroy
  * the entire KV cache" (Towards AI), "The Memory Math"; TurboQuant slides,
