@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libqjl.so")
 
 SOURCES = ["api.cu", "sketch_host.cu", "quantize_values.cu", "quantize_keys.cu", "quantize_keys_tc.cu", "decode.cu",
            "decode_static.cu", "merge.cu", "exact_decode.cu", "rope.cu", "cache_read.cu", "cache_commit.cu",
-           "tree_attention.cu"]
+           "tree_attention.cu", "tree_attention_tc.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

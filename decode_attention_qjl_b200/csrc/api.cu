@@ -687,7 +687,7 @@ size_t qjl_tree_attention_workspace_bytes(const qjl_ctx* ctx, int B, int N, int 
   if (static_cast<int64_t>(B) * Hkv > 65535) return 0;
   const int g = Hq / Hkv;
   if (g != 1 && g != 2 && g != 4 && g != 8) return 0;
-  return qjl::tree_ws_bytes(B, N, Hq, Hkv, ctx->m, ctx->m_out, ctx->num_sms);
+  return qjl::tree_ws_bytes(B, N, Hq, Hkv, ctx->m, ctx->m_out, ctx->vbits, ctx->num_sms);
 }
 
 qjl_status qjl_tree_attention(qjl_ctx* ctx, const qjl_cache* cache, const qjl_cache* draft, const void* Q,

@@ -1,0 +1,137 @@
+// tcgen05, mbarrier and bulk-copy wrappers of the tensor-core kernels of the
+// speculative step (tree_attention_tc.cu, cache_read.cu).
+#pragma once
+
+#include "qjl_internal.cuh"
+
+namespace qjl {
+namespace tc {
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool bar_wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit,
+                                           volatile int* err) {
+  const long long t0 = clock64();
+  for (;;) {
+    if (bar_try(bar, parity)) return true;
+    if (static_cast<unsigned long long>(clock64() - t0) > limit || (err && *err)) {
+      if (err) *err = 1;
+      return false;
+    }
+  }
+}
+// Wait for the phase with the given parity; false after `limit` SM clock
+// cycles, or once another waiter of the block has given up (*err).
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile int* err) {
+  return bar_try(bar, parity) || bar_wait_slow(bar, parity, limit, err);
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// 16 or 32 consecutive columns of this warp's 32 tensor-memory lanes, without the wait.
+__device__ __forceinline__ void ld16(uint32_t (&v)[16], uint32_t taddr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Shared-memory matrix descriptors in the 128-byte swizzle.
+// K-major: rows of 128 bytes (64 16-bit elements along K), 8-row groups 1024
+// bytes apart. MN-major: K rows of 128 bytes (64 elements along M or N), 8-row
+// groups `1024` bytes apart, blocks of 64 along M or N `lbo` bytes apart.
+__device__ __forceinline__ uint64_t desc_base() {
+  return (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+  return desc_base() | (static_cast<uint64_t>(1) << 16) | ((saddr >> 4) & 0x3FFFu);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
+  return desc_base() | (static_cast<uint64_t>(lbo >> 4) << 16) | ((saddr >> 4) & 0x3FFFu);
+}
+// Instruction descriptor of kind::f16 with an fp32 accumulator, M = 128: bf16
+// or fp16 operands, A and B K-major (0) or MN-major (1).
+__host__ __device__ constexpr uint32_t idesc_f16(int n, bool bf16, int a_mn, int b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+
+// Sign words as tensor-core operand: element e of the 32 of a word is `pos`
+// (a 16-bit pattern with a clear sign bit, in both halves) with the sign of
+// bit 15 - j (e = 2j) or 31 - j (e = 2j + 1): one shift and one three-input
+// logic operation per two elements.
+__device__ __forceinline__ void expand_word(uint32_t word, uint32_t pos2, uint32_t* out) {
+  const uint32_t neg = pos2 | 0x80008000u;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) out[j] = neg ^ ((word << j) & 0x80008000u);
+}
+// The element of a word's 32 that bit b becomes.
+__host__ __device__ inline int expand_pos(int b) { return b < 16 ? 2 * (15 - b) : 2 * (31 - b) + 1; }
+
+}  // namespace tc
+}  // namespace qjl

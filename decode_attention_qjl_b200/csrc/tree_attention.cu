@@ -1,4 +1,5 @@
-// Attention of drafted tokens over the QJL cache, in fp32 on the CUDA cores.
+// Attention of drafted tokens over the QJL cache, in fp32 on the CUDA cores (fp32
+// queries; bf16 ones take tree_attention_tc.cu).
 //
 // Rows: the N drafted tokens of a sequence times the G query heads of a kv
 // head, row r = i G + g. With the projected query sq (m + m_out values, the
@@ -47,20 +48,6 @@ TreeWs tree_ws_fp32(int B, int N, int Hq, int Hkv, int m, int m_out, int num_sms
   return w;
 }
 
-template <typename T>
-__device__ __forceinline__ float from_in(T x);
-template <>
-__device__ __forceinline__ float from_in<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float from_in<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T to_out(float x);
-template <>
-__device__ __forceinline__ float to_out<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-template <typename T>
 __global__ void __launch_bounds__(kTreeThreads) tree_project_kernel(TreeParams p, float* sq) {
   __shared__ float q[kHeadDim][kTreeRows];
   __shared__ bool outl[kHeadDim];
@@ -73,7 +60,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_project_kernel(TreeParams p
 #pragma unroll
   for (int k = 0; k < kTreeRows; ++k) {
     const int r = blockIdx.x * kTreeRows + k, i = r / p.G, g = r % p.G;
-    q[c][k] = i < p.N ? from_in(static_cast<const T*>(p.Q)[b * p.q_sb + i * p.q_sn + (hk * p.G + g) * p.q_sh + c]) : 0.0f;
+    q[c][k] = i < p.N ? static_cast<const float*>(p.Q)[b * p.q_sb + i * p.q_sn + (hk * p.G + g) * p.q_sh + c] : 0.0f;
   }
   __syncthreads();
   float* out = sq + (bh * rb + blockIdx.x) * static_cast<int64_t>(proj) * kTreeRows;
@@ -224,7 +211,6 @@ __global__ void __launch_bounds__(kTreeThreads) tree_chunk_kernel(TreeParams p, 
 }
 
 // One warp per output row (b, i, query head); lane l owns channels 4l .. 4l + 3.
-template <typename T>
 __global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p, const float* __restrict__ part_o,
                                                          const float* __restrict__ part_ml, int splits, int rb) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -251,15 +237,11 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p, const flo
     acc.w = fmaf(o.w, f, acc.w);
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  T* out = static_cast<T*>(p.O) + row * kHeadDim + 4 * lane;
-  out[0] = to_out<T>(acc.x * inv);
-  out[1] = to_out<T>(acc.y * inv);
-  out[2] = to_out<T>(acc.z * inv);
-  out[3] = to_out<T>(acc.w * inv);
+  reinterpret_cast<float4*>(static_cast<float*>(p.O) + row * kHeadDim)[lane] =
+      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
-template <typename T>
-cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
+cudaError_t launch_tree_fp32(const TreeParams& p, cudaStream_t s) {
   const int rb = tree_row_blocks(p.N, p.G);
   const int pairs = p.B * p.Hkv;
   const int splits = tree_splits(pairs, rb, p.num_sms);
@@ -267,25 +249,28 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
   float* sq = reinterpret_cast<float*>(p.ws + w.sq);
   float* part_o = reinterpret_cast<float*>(p.ws + w.part_o);
   float* part_ml = reinterpret_cast<float*>(p.ws + w.part_ml);
-  tree_project_kernel<T><<<dim3(rb, pairs), kTreeThreads, 0, s>>>(p, sq);
+  tree_project_kernel<<<dim3(rb, pairs), kTreeThreads, 0, s>>>(p, sq);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   tree_chunk_kernel<<<dim3(splits, rb, pairs), kTreeThreads, 0, s>>>(p, sq, part_o, part_ml);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.B) * p.N * p.Hq;
-  tree_merge_kernel<T><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(p, part_o, part_ml, splits, rb);
+  tree_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(p, part_o, part_ml, splits, rb);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t tree_ws_bytes(int B, int N, int Hq, int Hkv, int m, int m_out, int num_sms) {
-  return tree_ws_fp32(B, N, Hq, Hkv, m, m_out, num_sms).total;
+// One size for both dtypes: a workspace serves any call of its shape.
+size_t tree_ws_bytes(int B, int N, int Hq, int Hkv, int m, int m_out, int vbits, int num_sms) {
+  const size_t a = tree_ws_fp32(B, N, Hq, Hkv, m, m_out, num_sms).total;
+  const size_t b = tree_tc_ws_bytes(B, N, Hq, Hkv, m, m_out, vbits, num_sms);
+  return a > b ? a : b;
 }
 
 cudaError_t launch_tree_attention(const TreeParams& p, qjl_dtype dt, cudaStream_t s) {
-  return dt == QJL_BF16 ? launch_tree<__nv_bfloat16>(p, s) : launch_tree<float>(p, s);
+  return dt == QJL_BF16 ? launch_tree_attention_tc(p, s) : launch_tree_fp32(p, s);
 }
 
 }  // namespace qjl

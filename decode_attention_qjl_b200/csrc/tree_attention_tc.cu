@@ -1,0 +1,1002 @@
+// Attention of drafted tokens over the QJL cache on the tensor cores (bf16
+// queries).
+//
+// Rows r = i G + g of a (sequence, kv head): drafted token i, query head g of
+// the kv head. With sq the projected query of a row (the estimator's factors,
+// sm_scale and log2(e) folded in) the logits of 128 tokens are one product,
+//   X^T [token, row] = (signs * norm) [token, m + m_out] sq^T [m + m_out, row],
+// because the norm of a key is stored as fp16: a sign bit times the norm is an
+// fp16 number with that sign, exactly. Tokens are the M dimension of both
+// products, rows the N dimension, so that a few rows cost a few columns:
+//   O^T [dim, row] += V_hat^T [dim, token] P [token, row].
+// The sign operand is written to tensor memory by the threads that own its
+// tokens (lane = token), which keeps it out of shared memory.
+//
+// Roles of a persistent block (one per SM, all 512 tensor-memory columns):
+//   warps 0-3    signs and norms of 128 tokens -> tensor memory, 64 projections
+//                at a time (a ring of four)
+//   warps 4-7    value codes -> fp16 values in shared memory, thread = token
+//   warps 8-15   logits -> weights (fp16, shared memory), running maximum, sums
+//   warp 16      one thread issues every tcgen05.mma
+//   warp 17      bulk copies of cache tiles (two 64-token tiles a stage)
+// The work is the list of 128-token units of every (sequence, kv head, row
+// block), cut into equal contiguous ranges; what two blocks share is joined by
+// tree_join_kernel. The last unit of an item is the draft tile, the only one
+// with a mask.
+//
+// Softmax: p = 2^(x - ref) with ref = (maximum seen) - 8, moved only when a
+// logit passes ref + 15: weights stay below 2^15 in fp16, and those down to
+// 2^-22 of the largest keep all their bits. Values are kept as V_hat / 16,
+// which no fp16 scale and zero can push past the fp16 range. All sums are fp32.
+#include "tc_common.cuh"
+
+namespace qjl {
+namespace {
+
+using namespace tc;
+
+constexpr int kUnit = 128;              // tokens of a unit (MMA M)
+constexpr int kKWarps = 4, kVWarps = 4, kSWarps = 8;
+constexpr int kSWarp0 = kKWarps + kVWarps, kMmaWarp = kSWarp0 + kSWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kTreeTcThreads = 32 * (kLoadWarp + 1);
+constexpr int kARing = 4;               // sign operand chunks of 64 projections (32 columns)
+constexpr int kMaxStages = 4;
+constexpr int kColS = 0, kColO = 256, kColA = 384;  // tensor-memory columns: 2 x 128 logits, outputs, signs
+constexpr int kVBytes = kUnit * kHeadDim * 2;       // values of a unit
+constexpr int kPlane = kUnit * 128;                 // 64 rows' weights of a unit
+constexpr float kRefBelow = 8.0f, kRefMove = 15.0f;
+
+struct TreeTcCfg {
+  int rb;      // rows of a block (a multiple of 16, at most 128)
+  int nrb;     // row blocks of N * G rows
+  int nk;      // 64-projection chunks
+  int np;      // weight buffers
+  int ns;      // cache stages
+  int stage;   // bytes of a stage
+  int smem;
+};
+constexpr int kBadRing = 4;  // items whose drafted values may be in flight at once (three)
+constexpr int kMiscBytes = 3 * 128 * 4 + 4 * 128 * 4 + 128 * 8 + kBadRing * 64 * 4 + 40 * 8 + 64;
+
+// Row block, buffers and stages: the largest row block (fewest passes over the
+// cache) that leaves two stages, then a second weight buffer, then stages.
+TreeTcCfg tree_tc_cfg(int N, int G, int m, int m_out, int tile_bytes) {
+  TreeTcCfg c{};
+  const int R = N * G, limit = 227 * 1024 - 1024;
+  c.nk = (m + m_out + 63) / 64;
+  c.stage = 2 * tile_bytes;
+  for (int cap = 128;; cap -= 16) {
+    c.nrb = (R + cap - 1) / cap;
+    c.rb = ((R + c.nrb - 1) / c.nrb + 15) / 16 * 16;
+    const int planes = c.rb > 64 ? 2 : 1;
+    const int fixed = c.nk * c.rb * 128 + 2 * kVBytes + kMiscBytes;
+    c.np = 1;
+    c.ns = 2;
+    auto total = [&] { return fixed + c.np * planes * kPlane + c.ns * c.stage; };
+    if (total() > limit && cap > 16) continue;
+    c.np = 2;
+    if (total() > limit) c.np = 1;
+    while (c.ns < kMaxStages) {
+      ++c.ns;
+      if (total() > limit) {
+        --c.ns;
+        break;
+      }
+    }
+    c.smem = total() + 1024;
+    return c;
+  }
+}
+
+struct TreeTcWs {
+  size_t start, image, scale, part_o, part_ml, total;
+};
+TreeTcWs tree_tc_ws(const TreeTcCfg& c, int B, int Hkv, int num_sms) {
+  auto a256 = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t items = static_cast<size_t>(B) * Hkv * c.nrb;
+  TreeTcWs w{};
+  w.start = 0;
+  w.image = a256((static_cast<size_t>(B) + 1) * 8);
+  w.scale = w.image + a256(items * c.nk * c.rb * 128);
+  w.part_o = w.scale + a256(items * c.rb * 4);
+  w.part_ml = w.part_o + a256(static_cast<size_t>(2) * num_sms * c.rb * kHeadDim * 4);
+  w.total = w.part_ml + a256(static_cast<size_t>(2) * num_sms * c.rb * 8);
+  return w;
+}
+
+struct TreeTcParams {
+  TreeParams t;
+  TreeTcCfg c;
+  long long* start;      // [B + 1] first unit of each sequence
+  unsigned char* image;  // [B * Hkv][nrb] projected queries as the B operand
+  float* scale;          // [B * Hkv][nrb][rb] power-of-two scales of the rows
+  float* part_o;         // [2 * grid][rb][d]
+  float2* part_ml;       // [2 * grid][rb]
+  int grid;
+};
+
+__device__ __forceinline__ int seq_len(const TreeParams& t, int b) {
+  return t.seqlens ? min(max(t.seqlens[b], 0), t.T) : t.T;
+}
+__device__ __forceinline__ int seq_drafts(const TreeParams& t, int b) {
+  return t.n_draft ? min(max(t.n_draft[b], 0), t.N) : t.N;
+}
+__device__ __forceinline__ int seq_units(const TreeParams& t, int b) {  // units of one item of sequence b
+  return (seq_len(t, b) + kUnit - 1) / kUnit + 1;
+}
+__device__ __forceinline__ int seq_items(const TreeParams& t, const TreeTcCfg& c, int b) {
+  return t.Hkv * ((seq_drafts(t, b) * t.G + c.rb - 1) / c.rb);
+}
+
+// ---------------------------------------------------------------- preparation
+
+// Projected queries of 16 rows per block: sq = [S; S_out] q on bf16 MMAs (S in
+// decode's A-fragment order, products exact, fp32 sums), scaled so that the
+// row's largest entry lies in [2^14, 2^15), rounded to fp16 and written in the
+// order and swizzle of the score product's B operand. Block (0, 0) also writes
+// the first unit of every sequence.
+constexpr int kPrepWarps = 8;
+constexpr int kPrepWords = (kMaxM + kMaxMOut) / 32 / kPrepWarps;  // sign words of a warp
+
+__global__ void __launch_bounds__(32 * kPrepWarps) tree_prepare_kernel(TreeTcParams p) {
+  griddep_launch();
+  const TreeParams& t = p.t;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t bh = blockIdx.y;
+  const int b = static_cast<int>(bh / t.Hkv), hk = static_cast<int>(bh % t.Hkv);
+  if (blockIdx.x == 0 && bh == 0 && warp == 0) {
+    long long base = 0;
+    for (int b0 = 0; b0 < t.B; b0 += 32) {
+      const int bb = b0 + lane;
+      long long n = bb < t.B ? static_cast<long long>(seq_units(t, bb)) * seq_items(t, p.c, bb) : 0;
+      const long long own = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, n, off);
+        if (lane >= off) n += o;
+      }
+      if (bb < t.B) p.start[bb] = base + n - own;
+      base += __shfl_sync(0xffffffffu, n, 31);
+    }
+    if (lane == 0) p.start[t.B] = base;
+  }
+  const int nd = seq_drafts(t, b), live = nd * t.G;
+  const int row0 = blockIdx.x * 16;                    // rows of nrb * rb
+  if ((row0 / p.c.rb) * p.c.rb >= live) return;        // a row block nobody computes
+  __shared__ float top_s[kPrepWarps][16];
+  uint32_t om[4] = {0u, 0u, 0u, 0u};
+  {
+    const int c = lane < t.n_out ? min(max(t.idx[bh * t.n_out + lane], 0), kHeadDim - 1) : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) om[k] = __reduce_or_sync(0xffffffffu, c >= 0 && (c >> 5) == k ? 1u << (c & 31) : 0u);
+  }
+  // B fragments of the 16 rows (two 8-column tiles), inlier and outlier channels
+  const int q = lane & 3, r = lane >> 2;
+  uint32_t bf[2][8][2], keep[8][2];
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = 16 * ks + 8 * k + 2 * q;
+      const uint32_t o = (om[ks >> 1] >> (c & 31)) & 3u;
+      keep[ks][k] = (o & 1u ? 0u : 0x0000FFFFu) | (o & 2u ? 0u : 0xFFFF0000u);
+    }
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) {
+    const int row = row0 + 8 * nt + r, i = row / t.G, g = row % t.G;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(t.Q) + b * t.q_sb + i * t.q_sn +
+                               (static_cast<int64_t>(hk) * t.G + g) * t.q_sh;
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        bf[nt][ks][k] = row < live ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 * k + 2 * q) : 0u;
+  }
+  const int wpt = t.m / 32, words = wpt + t.m_out / 32;
+  float acc[kPrepWords][2][2][4];  // [word][16-row half][row tile]
+  float top[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+  for (int s = 0; s < kPrepWords; ++s) {
+    const int w = warp + kPrepWarps * s;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[s][hf][nt][k] = 0.0f;
+    if (w < words) {
+      const bool second = w >= wpt;
+      const float f = kSqrtHalfPi / static_cast<float>(second ? t.m_out : t.m) * t.sm_scale_log2;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint4 a = __ldg(t.S_frag + ((2 * w + hf) * 8 + ks) * 32 + lane);
+          const uint32_t k0 = second ? ~keep[ks][0] : keep[ks][0], k1 = second ? ~keep[ks][1] : keep[ks][1];
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            float* d = acc[s][hf][nt];
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                "{%0,%1,%2,%3};"
+                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(bf[nt][ks][0] & k0), "r"(bf[nt][ks][1] & k1));
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc[s][hf][nt][k] *= f;
+            top[nt][k & 1] = fmaxf(top[nt][k & 1], fabsf(acc[s][hf][nt][k]));
+          }
+      }
+    }
+  }
+  // the rows' largest entries: lanes 4r + q of a warp, then the warps
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float v = top[nt][k];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+      if (lane < 4) top_s[warp][8 * nt + 2 * q + k] = v;
+    }
+  __syncthreads();
+  unsigned char* img = p.image + (bh * p.c.nrb + row0 / p.c.rb) * static_cast<int64_t>(p.c.nk) * p.c.rb * 128;
+  const int in_block = row0 % p.c.rb;
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int col = 8 * nt + 2 * q + k;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kPrepWarps; ++w) v = fmaxf(v, top_s[w][col]);
+      // 2^e <= v < 2^(e+1): scale by 2^(14 - e), at most 2^126 (a row that small has logits of zero)
+      const int e = max(static_cast<int>(__float_as_uint(v) >> 23) - 127, -112);
+      const float up = v > 0.0f ? __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23) : 1.0f;
+      const float down = v > 0.0f ? __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) : 1.0f;
+      const int row = in_block + col;
+      if (warp == 0 && r == 0) p.scale[(bh * p.c.nrb + row0 / p.c.rb) * p.c.rb + row] = down;
+#pragma unroll
+      for (int s = 0; s < kPrepWords; ++s) {
+        const int w = warp + kPrepWarps * s;
+        if (w >= words) continue;
+        // bits r, r + 8 (half 0) and r + 16, r + 24 (half 1) of word w: elements 2j, 2j + 1 of j = 15 - r and 7 - r
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const __half2 h = __floats2half2_rn(acc[s][0][nt][2 * z + k] * up, acc[s][1][nt][2 * z + k] * up);
+          const int kk = 32 * (w & 1) + 2 * (15 - 8 * z - r);
+          *reinterpret_cast<uint32_t*>(img + (w >> 1) * p.c.rb * 128 + row * 128 + ((((kk >> 3) ^ row) & 7) << 4) +
+                                       (kk & 7) * 2) = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+    }
+}
+
+// ---------------------------------------------------------------- main kernel
+
+// The items (sequence, kv head, row block) of a block's range of units, in order.
+struct Walk {
+  int b, hk, rbk;            // current item
+  int len, nd, units, nblk;  // of sequence b
+  int u0, u1;                // this block's units of the item: [u0, u1) of `units`
+  long long left;            // units of the range from the current item's u0 on
+  __device__ bool begin(const TreeTcParams& p, long long first, long long end) {
+    left = end - first;
+    if (left <= 0) return false;
+    int lo = 0, hi = p.t.B - 1;  // the last sequence whose first unit is <= first (empty sequences share it)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.start[mid] <= first) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    load(p);
+    const long long off = first - p.start[b];
+    const int item = static_cast<int>(off / units);
+    hk = item / nblk;
+    rbk = item % nblk;
+    u0 = static_cast<int>(off % units);
+    u1 = static_cast<int>(min(static_cast<long long>(units), u0 + left));
+    return true;
+  }
+  __device__ void load(const TreeTcParams& p) {
+    len = seq_len(p.t, b);
+    nd = seq_drafts(p.t, b);
+    units = seq_units(p.t, b);
+    nblk = (nd * p.t.G + p.c.rb - 1) / p.c.rb;
+  }
+  __device__ bool next(const TreeTcParams& p) {
+    left -= u1 - u0;
+    if (left <= 0) return false;
+    if (++rbk >= nblk) {
+      rbk = 0;
+      if (++hk >= p.t.Hkv) {
+        hk = 0;
+        do ++b;
+        while (seq_drafts(p.t, b) == 0);  // units are left, so a sequence with drafts follows
+        load(p);
+      }
+    }
+    u0 = 0;
+    u1 = static_cast<int>(min(static_cast<long long>(units), left));
+    return true;
+  }
+  __device__ bool draft(int u) const { return u == units - 1; }
+  __device__ int tokens(int u) const { return draft(u) ? nd : min(kUnit, len - u * kUnit); }
+  __device__ int64_t bh(const TreeTcParams& p) const { return static_cast<int64_t>(b) * p.t.Hkv + hk; }
+};
+
+struct TreeTcSmem {
+  int sq, v, pw, raw, rowc, lsum, cmax, mask, bad, bars, misc;
+  __device__ explicit TreeTcSmem(const TreeTcCfg& c) {
+    sq = 0;
+    v = c.nk * c.rb * 128;
+    pw = v + 2 * kVBytes;
+    raw = pw + c.np * (c.rb > 64 ? 2 : 1) * kPlane;
+    rowc = raw + c.ns * c.stage;  // float [2][128]: scale and -ref of a row; float [128]: rescaling factor
+    cmax = rowc + 3 * 128 * 4;    // float [4][128]: column maxima, then sums, of the lane quarters
+    mask = cmax + 4 * 128 * 4;    // uint64 [128]
+    bad = mask + 128 * 8;         // uint32 [kBadRing][64]: value groups of a drafted token that are not finite
+    bars = bad + kBadRing * 64 * 4;
+    misc = bars + 40 * 8;
+  }
+};
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) { return f32x2_pack(a, b); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ bool s_any(bool x) {  // over the eight softmax warps
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred p, 1, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void s_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+
+// Reduces 16 values per lane over the 32 lanes, value k ending in lanes
+// 2 rev(k), 2 rev(k) + 1; returns the column of this lane.
+template <typename Op>
+__device__ __forceinline__ float reduce16(float (&v)[16], int lane, int* col, Op op) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int off = 16 >> s, n = 8 >> s;
+    const bool up = lane & off;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+      v[k] = op(keep, __shfl_xor_sync(0xffffffffu, send, off));
+    }
+  }
+  *col = (lane & 16 ? 8 : 0) + (lane & 8 ? 4 : 0) + (lane & 4 ? 2 : 0) + (lane & 2 ? 1 : 0);
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+
+__global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid_constant__ TreeTcParams p) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const TreeParams& t = p.t;
+  const TreeTcCfg& c = p.c;
+  const TreeTcSmem L(c);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L.bars);
+  uint64_t* raw_empty = raw_full + kMaxStages;
+  uint64_t* a_full = raw_empty + kMaxStages;
+  uint64_t* a_empty = a_full + kARing;
+  uint64_t* s_full = a_empty + kARing;
+  uint64_t* s_empty = s_full + 2;
+  uint64_t* p_full = s_empty + 2;
+  uint64_t* p_empty = p_full + 2;
+  uint64_t* v_full = p_empty + 2;
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* sq_full = v_empty + 2;
+  uint64_t* o_full = sq_full + 1;
+  uint64_t* o_empty = o_full + 1;
+  uint64_t* drain = o_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L.misc);
+  volatile int* err = reinterpret_cast<int*>(tmem_slot + 1);
+  if (tid == 0) {
+    for (int k = 0; k < kMaxStages; ++k) {
+      bar_init(&raw_full[k], 1);
+      bar_init(&raw_empty[k], kKWarps + kVWarps);
+    }
+    for (int k = 0; k < kARing; ++k) {
+      bar_init(&a_full[k], kKWarps);
+      bar_init(&a_empty[k], 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      bar_init(&s_full[k], 1);
+      bar_init(&s_empty[k], kSWarps);
+      bar_init(&p_full[k], kSWarps);
+      bar_init(&p_empty[k], 1);
+      bar_init(&v_full[k], kVWarps);
+      bar_init(&v_empty[k], 1);
+    }
+    bar_init(sq_full, 1);
+    bar_init(o_full, 1);
+    bar_init(o_empty, kSWarps);
+    bar_init(drain, 1);
+    *err = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();  // the projected queries and the unit table
+  griddep_launch();
+  const long long total = p.start[t.B];
+  const long long first = total * blockIdx.x / p.grid, end = total * (blockIdx.x + 1) / p.grid;
+  const unsigned long long limit = t.wait_cycles;
+  const unsigned long long limit_drain = limit > 2000000000ull ? limit : 2000000000ull;
+  Walk w;
+  const bool any = w.begin(p, first, end);
+
+  if (warp < kKWarps) {
+    // ============================================================ signs
+    const int tt = 32 * warp + lane, j = tt & 63;
+    const int wpt = t.m / 32, wpo = t.m_out / 32, words = wpt + wpo;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * warp) << 16) + kColA;
+    bool ok = true;
+    int st = 0, ring = 0;
+    uint32_t sph = 0, rph = 1;  // phases: stage full, chunk empty (the first pass finds every chunk empty)
+    for (bool more = any; more && ok; more = w.next(p))
+      for (int u = w.u0; u < w.u1 && ok; ++u) {
+        ok = bar_wait(&raw_full[st], sph, limit, err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const unsigned char* tile = smem + L.raw + st * c.stage + (tt >> 6) * t.tl.bytes;
+        const uint32_t norms = *reinterpret_cast<const uint32_t*>(tile + t.tl.knorm + 4 * j);
+        const uint32_t n_in = __byte_perm(norms, 0, 0x1010), n_out = __byte_perm(norms, 0, 0x3232);
+        const uint32_t* kb = reinterpret_cast<const uint32_t*>(tile + t.tl.kbits) + j * wpt;
+        const uint32_t* ko = reinterpret_cast<const uint32_t*>(tile + t.tl.kbits_out) + j * wpo - wpt;
+        for (int kc = 0; kc < c.nk; ++kc) {
+          const int w0 = 2 * kc, w1 = w0 + 1;
+          const uint32_t x0 = w0 < wpt ? kb[w0] : ko[w0];
+          const uint32_t x1 = w1 < wpt ? kb[w1] : w1 < words ? ko[w1] : 0u;
+          uint32_t e0[16], e1[16];
+          expand_word(x0, w0 < wpt ? n_in : n_out, e0);
+          expand_word(x1, w1 < wpt ? n_in : n_out, e1);
+          ok = bar_wait(&a_empty[ring], rph, limit, err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          fence_after();
+          st16(lane_addr + 32 * ring, e0);
+          st16(lane_addr + 32 * ring + 16, e1);
+          wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&a_full[ring]);
+          if (++ring == kARing) {
+            ring = 0;
+            rph ^= 1u;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&raw_empty[st]);
+        if (++st == c.ns) {
+          st = 0;
+          sph ^= 1u;
+        }
+      }
+  } else if (warp < kSWarp0) {
+    // ============================================================ values
+    const int tt = 32 * (warp - kKWarps) + lane, j = tt & 63;
+    uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L.bad);
+    bool ok = true;
+    int st = 0, vb = 0, item = 0;
+    uint32_t sph = 0, vph = 1;
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+    for (bool more = any; more && ok; more = w.next(p), ++item)
+      for (int u = w.u0; u < w.u1 && ok; ++u) {
+        ok = bar_wait(&raw_full[st], sph, limit, err) && bar_wait(&v_empty[vb], vph, limit, err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const unsigned char* tile = smem + L.raw + st * c.stage + (tt >> 6) * t.tl.bytes;
+        const bool live = tt < w.tokens(u), draft = w.draft(u);
+        const uint4 szv = *reinterpret_cast<const uint4*>(tile + t.tl.vsz + 16 * j);
+        const uint32_t sz[4] = {szv.x, szv.y, szv.z, szv.w};
+        unsigned char* row = smem + L.v + vb * kVBytes + tt * 128;
+        uint32_t bits = 0u;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          // a masked drafted value that is not finite must not meet a weight of
+          // zero in the product: it is left out here and added at the end
+          const bool off = draft && ((sz[g] & 0x7C00u) == 0x7C00u || (sz[g] & 0x7C000000u) == 0x7C000000u);
+          if (off) bits |= 1u << g;
+          const uint32_t use = live && !off ? sz[g] : 0u;
+          const __half2 s2 = __hmul2(__half2half2(__ushort_as_half(static_cast<unsigned short>(use))), sixteenth);
+          const __half2 z2 = __hmul2(__half2half2(__ushort_as_half(static_cast<unsigned short>(use >> 16))), sixteenth);
+          uint32_t lo[4], hi[4];  // codes of dims (8c + k, 8c + k + 4), k = 0..3, of 8-dim chunk c: two fields 16 bits apart
+          if (t.tl.vbits == 4) {
+            const uint4 cw = *reinterpret_cast<const uint4*>(tile + t.tl.vcode + j * (kHeadDim / 2) + 16 * vcode_chunk(j, g));
+            const uint32_t cc[4] = {cw.x, cw.y, cw.z, cw.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              lo[k] = cc[k];
+              hi[k] = cc[k] >> 8;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // two bits per code -> the nibble form: bits 0-1 and 2-3 of each byte to bits 0 and 4 of a half word
+              const uint32_t x = static_cast<uint32_t>(tile[t.tl.vcode + v2_line(g, 2 * k) + j]) |
+                                 (static_cast<uint32_t>(tile[t.tl.vcode + v2_line(g, 2 * k + 1) + j]) << 16);
+              lo[k] = (x & 0x00030003u) | ((x & 0x000C000Cu) << 2);
+              hi[k] = ((x >> 4) & 0x00030003u) | ((x & 0x00C000C0u) >> 2);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // 0x6400 | n is 1024 + n, and with the code four bits up 1024 + 16 n
+            uint32_t y[4];
+            const uint32_t f[4] = {(lo[k] & 0x000F000Fu) | 0x64006400u, (lo[k] & 0x00F000F0u) | 0x64006400u,
+                                   (hi[k] & 0x000F000Fu) | 0x64006400u, (hi[k] & 0x00F000F0u) | 0x64006400u};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 h = *reinterpret_cast<const __half2*>(&f[e]);
+              const __half2 n = e & 1 ? __hfma2(h, sixteenth, __float2half2_rn(-64.0f)) : __hsub2(h, __float2half2_rn(1024.0f));
+              const __half2 r = __hfma2(n, s2, z2);
+              y[e] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+            const int ch = 4 * g + k;  // 8-dim chunk
+            *reinterpret_cast<uint4*>(row + (ch >> 3) * kPlane + (((ch ^ tt) & 7) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+        if (draft && tt < 64) bad[64 * (item % kBadRing) + tt] = live ? bits : 0u;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&v_full[vb]);
+          bar_arrive(&raw_empty[st]);
+        }
+        vb ^= 1;
+        if (vb == 0) vph ^= 1u;
+        if (++st == c.ns) {
+          st = 0;
+          sph ^= 1u;
+        }
+      }
+  } else if (warp < kMmaWarp) {
+    // ============================================================ weights
+    const int quarter = warp & 3, half = (warp - kSWarp0) >> 2, tt = 32 * quarter + lane, stid = tid - 32 * kSWarp0;
+    const int nb = c.rb / 16;  // 16-row groups; this warp takes those of parity `half`
+    float* sc = reinterpret_cast<float*>(smem + L.rowc);
+    float* nref = sc + 128;
+    float* fac = nref + 128;
+    float* cmax = reinterpret_cast<float*>(smem + L.cmax);
+    uint64_t* mrow = reinterpret_cast<uint64_t*>(smem + L.mask);
+    const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + L.bad);
+    const uint32_t laddr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    const int planes = c.rb > 64 ? 2 : 1;
+    bool ok = true;
+    int n = 0;            // units so far
+    uint32_t oph = 0;
+    int it = 0;
+    for (bool more = any; more; more = w.next(p), ++it) {
+      const int64_t item = w.bh(p) * c.nrb + w.rbk;
+      uint64_t lsum[4][8];  // sums of this token's weights, pairs of rows
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) lsum[i][k] = 0ull;
+      if (stid < c.rb) {
+        const int row = w.rbk * c.rb + stid, i = row / t.G;
+        sc[stid] = p.scale[item * c.rb + stid];
+        nref[stid] = INFINITY;  // -ref of "nothing seen"
+        mrow[stid] = i >= w.nd ? 0ull
+                     : t.mask ? t.mask[static_cast<int64_t>(w.b) * t.N + i]
+                     : i == 63 ? ~0ull : (2ull << i) - 1ull;
+      }
+      s_sync();
+      for (int u = w.u0; u < w.u1; ++u, ++n) {
+        const bool first_u = u == w.u0, draft = w.draft(u), live = tt < w.tokens(u);
+        if (ok) ok = bar_wait(&s_full[n & 1], (n >> 1) & 1, limit, err);
+        ok = __all_sync(0xffffffffu, ok);
+        fence_after();
+        const uint32_t saddr = laddr + kColS + 128 * (n & 1);
+        bool move = first_u;
+        if (!first_u) {  // does any logit pass its row's ref + 15?
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int blk = 2 * i + half;
+            if (blk < nb) {
+              uint32_t v[16];
+              ld16(v, saddr + 16 * blk);
+              wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const uint64_t s2 = *reinterpret_cast<const uint64_t*>(sc + 16 * blk + k);
+                const uint64_t r2 = *reinterpret_cast<const uint64_t*>(nref + 16 * blk + k);
+                uint64_t x;
+                asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"((static_cast<uint64_t>(v[k + 1]) << 32) | v[k]), "l"(s2), "l"(r2));
+                float a = f32x2_lo(x), b = f32x2_hi(x);
+                if (draft) {
+                  if (!((mrow[16 * blk + k] >> (tt & 63)) & 1ull)) a = -INFINITY;
+                  if (!((mrow[16 * blk + k + 1] >> (tt & 63)) & 1ull)) b = -INFINITY;
+                }
+                top = fmaxf(top, fmaxf(a, b));
+              }
+            }
+          }
+          move = s_any(live && top > kRefMove);
+        }
+        if (move) {
+          // column maxima of this unit
+#pragma unroll 1
+          for (int blk = half; blk < nb; blk += 2) {
+            uint32_t v[16];
+            ld16(v, saddr + 16 * blk);
+            wait_ld();
+            float x[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              x[k] = __uint_as_float(v[k]) * sc[16 * blk + k];
+              if (!live || (draft && !((mrow[16 * blk + k] >> (tt & 63)) & 1ull))) x[k] = -INFINITY;
+            }
+            int col;
+            const float m = reduce16(x, lane, &col, [](float a, float b) { return fmaxf(a, b); });
+            if (!(lane & 1)) cmax[128 * quarter + 16 * blk + col] = m;
+          }
+          s_sync();
+          if (stid < c.rb) {
+            const float m = fmaxf(fmaxf(cmax[stid], cmax[128 + stid]), fmaxf(cmax[256 + stid], cmax[384 + stid]));
+            const float old = nref[stid];                          // -ref, +inf: nothing seen
+            const float now = m == -INFINITY ? old : fminf(old, kRefBelow - m);
+            nref[stid] = now;
+            fac[stid] = now == old ? 1.0f : ex2(now - old);  // 2^(old ref - new ref); nothing seen: 0
+          }
+          s_sync();
+          if (!first_u) {
+            // the sums and outputs so far, relative to the new references
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int blk = 2 * i + half;
+              if (blk < nb)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float2 f = *reinterpret_cast<const float2*>(fac + 16 * blk + 2 * k);
+                  lsum[i][k] = pack2(f32x2_lo(lsum[i][k]) * f.x, f32x2_hi(lsum[i][k]) * f.y);
+                }
+            }
+            const int q = n - 1;  // the last product into the outputs
+            if (ok) ok = bar_wait(&p_empty[q % c.np], (q / c.np) & 1, limit, err);
+            ok = __all_sync(0xffffffffu, ok);
+            fence_after();
+#pragma unroll 1
+            for (int blk = half; blk < nb; blk += 2) {
+              uint32_t v[16];
+              ld16(v, laddr + kColO + 16 * blk);
+              wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * fac[16 * blk + k]);
+              st16(laddr + kColO + 16 * blk, v);
+            }
+            wait_st();
+          }
+        }
+        // weights
+        const int pb = n % c.np;
+        if (n >= c.np) {
+          if (ok) ok = bar_wait(&p_empty[pb], (n / c.np - 1) & 1, limit, err);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        unsigned char* prow = smem + L.pw + pb * planes * kPlane + tt * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int blk = 2 * i + half;
+          if (blk < nb) {
+            uint32_t v[16];
+            ld16(v, saddr + 16 * blk);
+            wait_ld();
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const uint64_t s2 = *reinterpret_cast<const uint64_t*>(sc + 16 * blk + k);
+              const uint64_t r2 = *reinterpret_cast<const uint64_t*>(nref + 16 * blk + k);
+              uint64_t x;
+              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"((static_cast<uint64_t>(v[k + 1]) << 32) | v[k]), "l"(s2), "l"(r2));
+              float a = ex2(f32x2_lo(x)), b = ex2(f32x2_hi(x));
+              if (!live) a = b = 0.0f;
+              if (draft) {
+                if (!((mrow[16 * blk + k] >> (tt & 63)) & 1ull)) a = 0.0f;
+                if (!((mrow[16 * blk + k + 1] >> (tt & 63)) & 1ull)) b = 0.0f;
+              }
+              asm("add.rn.f32x2 %0, %1, %2;" : "=l"(lsum[i][k >> 1]) : "l"(lsum[i][k >> 1]), "l"(pack2(a, b)));
+              const __half2 hh = __floats2half2_rn(a, b);
+              h[k >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            unsigned char* dst = prow + (blk >> 2) * kPlane;
+            const int c0 = 2 * (blk & 3);
+            *reinterpret_cast<uint4*>(dst + (((c0 ^ tt) & 7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + ((((c0 + 1) ^ tt) & 7) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+        }
+        fence_async_smem();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&s_empty[n & 1]);
+          bar_arrive(&p_full[pb]);
+        }
+      }
+      // ---- the item's end: sums over the tokens, outputs
+      s_sync();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int blk = 2 * i + half;
+        if (blk < nb) {
+          float x[16];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x[2 * k] = f32x2_lo(lsum[i][k]);
+            x[2 * k + 1] = f32x2_hi(lsum[i][k]);
+          }
+          int col;
+          const float s = reduce16(x, lane, &col, [](float a, float b) { return a + b; });
+          if (!(lane & 1)) cmax[128 * quarter + 16 * blk + col] = s;
+        }
+      }
+      if (ok) ok = bar_wait(o_full, oph, limit, err);
+      oph ^= 1u;
+      ok = __all_sync(0xffffffffu, ok);
+      const bool fine = !s_any(!ok);
+      fence_after();
+      const bool whole = w.u0 == 0 && w.u1 == w.units;
+      const bool has_draft = w.u1 == w.units;
+      const long long item_start = first + ((end - first) - w.left) - w.u0;  // first unit of the item
+      const int slot = 2 * blockIdx.x + (first < item_start ? 1 : 0);
+      // tensor-memory lane -> dim: values were paired four dims apart
+      const int dim = (tt & ~7) + ((tt & 7) >> 1) + 4 * (tt & 1);
+#pragma unroll 1
+      for (int blk = half; blk < nb; blk += 2) {
+        uint32_t v[16];
+        ld16(v, laddr + kColO + 16 * blk);
+        wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int col = 16 * blk + k, row = w.rbk * c.rb + col, i = row / t.G, g = row % t.G;
+          if (i >= w.nd) continue;
+          const float sum = (cmax[col] + cmax[128 + col]) + (cmax[256 + col] + cmax[384 + col]);
+          float o = __uint_as_float(v[k]) * 16.0f;
+          if (has_draft)  // drafted values that are not finite
+            for (int d = 0; d < w.nd; ++d) {
+              const uint32_t bb = bad[64 * (it % kBadRing) + d];
+              if (bb != 0u && ((bb >> (dim >> 5)) & 1u) && ((mrow[col] >> d) & 1ull)) o += __int_as_float(0x7fc00000);
+            }
+          if (!fine) o = __int_as_float(0x7fc00000);
+          if (whole) {
+            const float inv = sum == 0.0f && fine ? 0.0f : 1.0f / sum;
+            static_cast<__nv_bfloat16*>(t.O)[((static_cast<int64_t>(w.b) * t.N + i) * t.Hq + w.hk * t.G + g) * kHeadDim + dim] =
+                __float2bfloat16_rn(sum == 0.0f && fine ? 0.0f : o * inv);
+          } else {
+            p.part_o[(static_cast<int64_t>(slot) * c.rb + col) * kHeadDim + dim] = o;
+            if (tt == 0) p.part_ml[slot * c.rb + col] = make_float2(-nref[col], fine ? sum : __int_as_float(0x7fc00000));
+          }
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(o_empty);
+      s_sync();  // the row constants and sums may be overwritten
+    }
+  } else if (warp == kMmaWarp) {
+    // ============================================================ products
+    if (lane == 0) {
+      bool ok = true;
+      int n = 0, ring = 0, item = 0;
+      uint32_t aph = 0;
+      const uint32_t sq_base = smem_u32(smem + L.sq), v_base = smem_u32(smem + L.v), p_base = smem_u32(smem + L.pw);
+      const int planes = c.rb > 64 ? 2 : 1;
+      const uint32_t id_s = idesc_f16(c.rb, false, 0, 0), id_o = idesc_f16(c.rb, false, 1, 1);
+      const int ksteps = (t.m + t.m_out) / 16;
+      const uint32_t sq_bytes = static_cast<uint32_t>(c.nk) * c.rb * 128;
+      bool sq_out = false;  // a copy of the projected queries is in flight
+      auto values = [&](int q, bool first_u, bool last_u) {  // O += V^T P of unit q
+        const int pb = q % c.np, vb = q & 1;
+        ok = ok && bar_wait(&p_full[pb], (q / c.np) & 1, limit, err) && bar_wait(&v_full[vb], (q >> 1) & 1, limit, err);
+        if (ok && first_u && item > 0) ok = bar_wait(o_empty, (item - 1) & 1, limit, err);
+        if (!ok) return;
+        fence_after();
+#pragma unroll
+        for (int ks = 0; ks < kUnit / 16; ++ks)
+          mma_ss(tmem + kColO, desc_mn(v_base + vb * kVBytes + ks * 2048, kPlane),
+                 desc_mn(p_base + pb * planes * kPlane + ks * 2048, kPlane), id_o, !(first_u && ks == 0));
+        commit(&p_empty[pb]);
+        commit(&v_empty[vb]);
+        if (last_u) commit(o_full);
+      };
+      for (bool more = any; more && ok; more = w.next(p), ++item) {
+        // the last item's score products are done: its logits were read (s_full was waited for by the weights, and
+        // `values` of its last unit waited for those)
+        bar_expect(sq_full, sq_bytes);
+        bulk_load(sq_base, p.image + (w.bh(p) * c.nrb + w.rbk) * static_cast<int64_t>(sq_bytes), sq_bytes, sq_full);
+        sq_out = true;
+        ok = bar_wait(sq_full, item & 1, limit, err);
+        if (!ok) break;
+        sq_out = false;
+        for (int u = w.u0; u < w.u1 && ok; ++u, ++n) {
+          if (n >= 2) ok = bar_wait(&s_empty[n & 1], ((n >> 1) - 1) & 1, limit, err);
+          for (int kc = 0; kc < c.nk && ok; ++kc) {
+            ok = bar_wait(&a_full[ring], aph, limit, err);
+            if (!ok) break;
+            fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              if (4 * kc + ks < ksteps)
+                mma_ts(tmem + kColS + 128 * (n & 1), tmem + kColA + 32 * ring + 8 * ks,
+                       desc_k(sq_base + kc * c.rb * 128 + 32 * ks), id_s, kc + ks > 0);
+            commit(&a_empty[ring]);
+            if (++ring == kARing) {
+              ring = 0;
+              aph ^= 1u;
+            }
+          }
+          if (!ok) break;
+          commit(&s_full[n & 1]);
+          if (u > w.u0) values(n - 1, u - 1 == w.u0, false);
+        }
+        if (ok) values(n - 1, w.u1 - 1 == w.u0, true);
+      }
+      // every product issued here ends before the block gives its memory back
+      commit(drain);
+      bar_wait(drain, 0, limit_drain, nullptr);
+      if (sq_out) bar_wait(sq_full, item & 1, limit_drain, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ============================================================ cache tiles
+    if (lane == 0) {
+      bool ok = true;
+      int st = 0, issued = 0;
+      uint32_t eph = 1;
+      for (bool more = any; more && ok; more = w.next(p)) {
+        const int64_t bh = w.bh(p);
+        for (int u = w.u0; u < w.u1; ++u) {
+          ok = bar_wait(&raw_empty[st], eph, limit, err);
+          if (!ok) break;
+          const unsigned char* src;
+          int tiles = 1;
+          if (w.draft(u)) {
+            src = t.draft + bh * (t.draft_cap / kDecodeTileTokens) * static_cast<int64_t>(t.tl.bytes);
+          } else {
+            src = t.tiles + (bh * (t.cap / kDecodeTileTokens) + 2 * u) * static_cast<int64_t>(t.tl.bytes);
+            tiles = w.len - u * kUnit > kDecodeTileTokens ? 2 : 1;
+          }
+          const uint32_t bytes = static_cast<uint32_t>(tiles * t.tl.bytes);
+          bar_expect(&raw_full[st], bytes);
+          bulk_load(smem_u32(smem + L.raw + st * c.stage), src, bytes, &raw_full[st]);
+          ++issued;
+          if (++st == c.ns) {
+            st = 0;
+            eph ^= 1u;
+          }
+        }
+      }
+      // every copy issued here lands before the block gives its memory back
+      for (int q = issued > c.ns ? issued - c.ns : 0; q < issued; ++q)
+        bar_wait(&raw_full[q % c.ns], (q / c.ns) & 1, limit_drain, nullptr);
+    }
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// ---------------------------------------------------------------- join
+
+// One warp per output row: rows past the drafts are zero, rows of an item that
+// one block held whole are already written, the others are joined from the
+// parts of the blocks cta(u0) .. cta(u1 - 1) that share the item.
+__global__ void __launch_bounds__(256) tree_join_kernel(TreeTcParams p) {
+  griddep_wait();
+  const TreeParams& t = p.t;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= static_cast<int64_t>(t.B) * t.N * t.Hq) return;
+  const int h = static_cast<int>(row % t.Hq), i = static_cast<int>(row / t.Hq % t.N);
+  const int b = static_cast<int>(row / t.Hq / t.N);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(t.O) + row * kHeadDim + 4 * lane;
+  if (i >= seq_drafts(t, b)) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
+    return;
+  }
+  const int r = i * t.G + h % t.G, units = seq_units(t, b);
+  const int nblk = (seq_drafts(t, b) * t.G + p.c.rb - 1) / p.c.rb;
+  const long long u0 = p.start[b] + (static_cast<long long>(h / t.G) * nblk + r / p.c.rb) * units;
+  const long long total = p.start[t.B];
+  const long long c0 = ((u0 + 1) * p.grid - 1) / total, c1 = ((u0 + units) * p.grid - 1) / total;
+  if (c0 == c1) return;
+  const int col = r % p.c.rb;
+  auto slot = [&](long long c) { return 2 * c + (total * c / p.grid < u0 ? 1 : 0); };
+  // (with fewer units than blocks some of them have none)
+  auto idle = [&](long long c) { return total * (c + 1) / p.grid == total * c / p.grid; };
+  float M = -INFINITY, L = 0.0f;
+  for (long long c = c0; c <= c1; ++c)
+    if (!idle(c)) M = fmaxf(M, p.part_ml[slot(c) * p.c.rb + col].x);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (long long c = c0; c <= c1; ++c) {
+    if (idle(c)) continue;
+    const int64_t s = slot(c) * p.c.rb + col;
+    const float2 ml = p.part_ml[s];
+    if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // nothing seen (a NaN sum stays)
+    const float f = ml.x == M ? 1.0f : exp2f(ml.x - M);
+    const float4 o = reinterpret_cast<const float4*>(p.part_o)[s * (kHeadDim / 4) + lane];
+    L = fmaf(ml.y, f, L);
+    acc.x = fmaf(o.x, f, acc.x);
+    acc.y = fmaf(o.y, f, acc.y);
+    acc.z = fmaf(o.z, f, acc.z);
+    acc.w = fmaf(o.w, f, acc.w);
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+}  // namespace
+
+size_t tree_tc_ws_bytes(int B, int N, int Hq, int Hkv, int m, int m_out, int vbits, int num_sms) {
+  return tree_tc_ws(tree_tc_cfg(N, Hq / Hkv, m, m_out, tile_layout(m, m_out, vbits).bytes), B, Hkv, num_sms).total;
+}
+
+cudaError_t launch_tree_attention_tc(const TreeParams& t, cudaStream_t s) {
+  TreeTcParams p{};
+  p.t = t;
+  p.c = tree_tc_cfg(t.N, t.G, t.m, t.m_out, t.tl.bytes);
+  if (p.c.smem > 227 * 1024) return cudaErrorInvalidConfiguration;
+  const TreeTcWs w = tree_tc_ws(p.c, t.B, t.Hkv, t.num_sms);
+  p.start = reinterpret_cast<long long*>(t.ws + w.start);
+  p.image = t.ws + w.image;
+  p.scale = reinterpret_cast<float*>(t.ws + w.scale);
+  p.part_o = reinterpret_cast<float*>(t.ws + w.part_o);
+  p.part_ml = reinterpret_cast<float2*>(t.ws + w.part_ml);
+  const int64_t units = (static_cast<int64_t>(t.T) + kUnit - 1) / kUnit + 1;
+  const int64_t most = static_cast<int64_t>(t.B) * t.Hkv * p.c.nrb * units;
+  p.grid = static_cast<int>(most < t.num_sms ? most : t.num_sms);
+  // one block per SM: it takes all tensor-memory columns
+  const size_t smem = p.c.smem < 116 * 1024 ? 116 * 1024 : static_cast<size_t>(p.c.smem);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(tree_tc_kernel), smem);
+  if (e != cudaSuccess) return e;
+  tree_prepare_kernel<<<dim3(static_cast<unsigned>(p.c.nrb * p.c.rb / 16), static_cast<unsigned>(t.B * t.Hkv)),
+                        32 * kPrepWarps, 0, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
+  cfg.blockDim = dim3(kTreeTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tree_tc_kernel, p);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(t.B) * t.N * t.Hq;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel, p);
+}
+
+}  // namespace qjl
