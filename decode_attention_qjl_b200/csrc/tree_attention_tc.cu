@@ -13,20 +13,20 @@
 // tokens (lane = token), which keeps it out of shared memory.
 //
 // Roles of a persistent block (one per SM, all 512 tensor-memory columns):
-//   warps 0-3    signs and norms of 128 tokens -> tensor memory, 64 projections
-//                at a time (a ring of four)
+//   warps 0-3    signs and norms of 128 tokens -> tensor memory, 128 projections
+//                at a time (a ring of two)
 //   warps 4-7    value codes -> fp16 values in shared memory, thread = token
 //   warps 8-15   logits -> weights (fp16, shared memory), running maximum, sums
-//   warp 16      one thread issues every tcgen05.mma
+//   warp 16      issues every tcgen05.mma
 //   warp 17      bulk copies of cache tiles (two 64-token tiles a stage)
 // The work is the list of 128-token units of every (sequence, kv head, row
 // block), cut into equal contiguous ranges; what two blocks share is joined by
 // tree_join_kernel. The last unit of an item is the draft tile, the only one
 // with a mask.
 //
-// Softmax: p = 2^(x - ref) with ref = (maximum seen) - 8, moved only when a
+// Softmax: p = 2^(x - ref) with ref = (maximum seen) - 4, moved only when a
 // logit passes ref + 15: weights stay below 2^15 in fp16, and those down to
-// 2^-22 of the largest keep all their bits. Values are kept as V_hat / 16,
+// 2^-18 of the largest keep all their bits. Values are kept as V_hat / 16,
 // which no fp16 scale and zero can push past the fp16 range. All sums are fp32.
 #include "tc_common.cuh"
 
@@ -38,13 +38,16 @@ using namespace tc;
 constexpr int kUnit = 128;              // tokens of a unit (MMA M)
 constexpr int kKWarps = 4, kVWarps = 4, kSWarps = 8;
 constexpr int kSWarp0 = kKWarps + kVWarps, kMmaWarp = kSWarp0 + kSWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kTreeTcThreads = 32 * (kLoadWarp + 1);
-constexpr int kARing = 4;               // sign operand chunks of 64 projections (32 columns)
+constexpr int kTreeTcThreads = 640;      // five warpgroups; two warps of the last are idle
+// Registers per thread of the roles (setmaxnreg): 128 * (72 + 72 + 2 * 136 + 64) = 640 * 96, what the launch holds.
+constexpr int kRegsExpand = 72, kRegsWeights = 136, kRegsIssue = 64;
+constexpr int kARing = 2;               // sign operand chunks of 128 projections (64 columns)
 constexpr int kMaxStages = 4;
 constexpr int kColS = 0, kColO = 256, kColA = 384;  // tensor-memory columns: 2 x 128 logits, outputs, signs
 constexpr int kVBytes = kUnit * kHeadDim * 2;       // values of a unit
 constexpr int kPlane = kUnit * 128;                 // 64 rows' weights of a unit
-constexpr float kRefBelow = 8.0f, kRefMove = 15.0f;
+constexpr float kRefBelow = 4.0f, kRefMove = 15.0f;
+constexpr float kNothing = 3.0e38f;                 // -ref of a row that has seen nothing
 
 struct TreeTcCfg {
   int rb;      // rows of a block (a multiple of 16, at most 128)
@@ -277,7 +280,8 @@ __global__ void __launch_bounds__(32 * kPrepWarps) tree_prepare_kernel(TreeTcPar
 
 // ---------------------------------------------------------------- main kernel
 
-// The items (sequence, kv head, row block) of a block's range of units, in order.
+// The items (sequence, kv head, row block) of a block's range of units, in order
+// (walked by whole warps).
 struct Walk {
   int b, hk, rbk;            // current item
   int len, nd, units, nblk;  // of sequence b
@@ -298,8 +302,8 @@ struct Walk {
     const int item = static_cast<int>(off / units);
     hk = item / nblk;
     rbk = item % nblk;
-    u0 = static_cast<int>(off % units);
-    u1 = static_cast<int>(min(static_cast<long long>(units), u0 + left));
+    u0 = __shfl_sync(0xffffffffu, static_cast<int>(off % units), 0);
+    u1 = __shfl_sync(0xffffffffu, static_cast<int>(min(static_cast<long long>(units), u0 + left)), 0);
     return true;
   }
   __device__ void load(const TreeTcParams& p) {
@@ -321,7 +325,7 @@ struct Walk {
       }
     }
     u0 = 0;
-    u1 = static_cast<int>(min(static_cast<long long>(units), left));
+    u1 = __shfl_sync(0xffffffffu, static_cast<int>(min(static_cast<long long>(units), left)), 0);
     return true;
   }
   __device__ bool draft(int u) const { return u == units - 1; }
@@ -336,7 +340,7 @@ struct TreeTcSmem {
     v = c.nk * c.rb * 128;
     pw = v + 2 * kVBytes;
     raw = pw + c.np * (c.rb > 64 ? 2 : 1) * kPlane;
-    rowc = raw + c.ns * c.stage;  // float [2][128]: scale and -ref of a row; float [128]: rescaling factor
+    rowc = raw + c.ns * c.stage;  // float4 [64]: scales and -refs of two rows; float [128]: rescaling factor
     cmax = rowc + 3 * 128 * 4;    // float [4][128]: column maxima, then sums, of the lane quarters
     mask = cmax + 4 * 128 * 4;    // uint64 [128]
     bad = mask + 128 * 8;         // uint32 [kBadRing][64]: value groups of a drafted token that are not finite
@@ -351,19 +355,20 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ bool s_any(bool x) {  // over the eight softmax warps
+// The four weight warps that share their rows synchronise on their own barrier.
+__device__ __forceinline__ bool s_any(int half, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.or.pred p, 1, 256, q;\n\t"
+      "barrier.cta.red.or.pred p, %2, 128, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"(x ? 1u : 0u)
+      : "r"(x ? 1u : 0u), "r"(1 + half)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void s_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void s_sync(int half) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 
 // Reduces 16 values per lane over the 32 lanes, value k ending in lanes
 // 2 rev(k), 2 rev(k) + 1; returns the column of this lane.
@@ -383,13 +388,26 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, int* col, Op
   return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
+// Logits that do not count become -inf: dead tokens, and in the draft tile
+// what the rows' masks leave out.
+template <int N>
+__device__ __forceinline__ void mask16(uint32_t (&v)[N], int at, const uint64_t* mrow, int tt, bool live, bool draft) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if (!live || (draft && !((mrow[k] >> (tt & 63)) & 1ull))) v[at + k] = 0xFF800000u;
+}
+
+// NBW: 16-row groups of a weight warp.
+template <int NBW>
 __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid_constant__ TreeTcParams p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const TreeParams& t = p.t;
   const TreeTcCfg& c = p.c;
   const TreeTcSmem L(c);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp index, and below what a role's warp walks over, as uniform values: addresses and operands then take the
+  // uniform datapath
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L.bars);
   uint64_t* raw_empty = raw_full + kMaxStages;
   uint64_t* a_full = raw_empty + kMaxStages;
@@ -438,7 +456,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   griddep_wait();  // the projected queries and the unit table
   griddep_launch();
   const long long total = p.start[t.B];
@@ -450,8 +468,10 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
 
   if (warp < kKWarps) {
     // ============================================================ signs
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
     const int tt = 32 * warp + lane, j = tt & 63;
     const int wpt = t.m / 32, wpo = t.m_out / 32, words = wpt + wpo;
+    const bool even = ((wpt | wpo) & 1) == 0;  // word pairs are 8-byte aligned and of one part
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * warp) << 16) + kColA;
     bool ok = true;
     int st = 0, ring = 0;
@@ -466,27 +486,37 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         const uint32_t n_in = __byte_perm(norms, 0, 0x1010), n_out = __byte_perm(norms, 0, 0x3232);
         const uint32_t* kb = reinterpret_cast<const uint32_t*>(tile + t.tl.kbits) + j * wpt;
         const uint32_t* ko = reinterpret_cast<const uint32_t*>(tile + t.tl.kbits_out) + j * wpo - wpt;
-        for (int kc = 0; kc < c.nk; ++kc) {
-          const int w0 = 2 * kc, w1 = w0 + 1;
-          const uint32_t x0 = w0 < wpt ? kb[w0] : ko[w0];
-          const uint32_t x1 = w1 < wpt ? kb[w1] : w1 < words ? ko[w1] : 0u;
-          uint32_t e0[16], e1[16];
-          expand_word(x0, w0 < wpt ? n_in : n_out, e0);
-          expand_word(x1, w1 < wpt ? n_in : n_out, e1);
+#pragma unroll 1
+        for (int kc = 0; kc < c.nk; kc += 2) {
           ok = bar_wait(&a_empty[ring], rph, limit, err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           fence_after();
-          st16(lane_addr + 32 * ring, e0);
-          st16(lane_addr + 32 * ring + 16, e1);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int w0 = 2 * (kc + half), w1 = w0 + 1;
+            if (w0 >= words) continue;
+            uint32_t x0, x1;
+            if (even) {
+              const uint2 x = *reinterpret_cast<const uint2*>((w0 < wpt ? kb : ko) + w0);
+              x0 = x.x;
+              x1 = x.y;
+            } else {
+              x0 = w0 < wpt ? kb[w0] : ko[w0];
+              x1 = w1 < wpt ? kb[w1] : w1 < words ? ko[w1] : 0u;
+            }
+            uint32_t e[16];
+            expand_word(x0, w0 < wpt ? n_in : n_out, e);
+            st16(lane_addr + 64 * ring + 32 * half, e);
+            expand_word(x1, w1 < wpt ? n_in : n_out, e);
+            st16(lane_addr + 64 * ring + 32 * half + 16, e);
+          }
           wait_st();
           fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(&a_full[ring]);
-          if (++ring == kARing) {
-            ring = 0;
-            rph ^= 1u;
-          }
+          ring ^= 1;
+          rph ^= ring == 0 ? 1u : 0u;
         }
         __syncwarp();
         if (lane == 0) bar_arrive(&raw_empty[st]);
@@ -497,6 +527,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       }
   } else if (warp < kSWarp0) {
     // ============================================================ values
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
     const int tt = 32 * (warp - kKWarps) + lane, j = tt & 63;
     uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L.bad);
     bool ok = true;
@@ -510,17 +541,17 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         if (!ok) break;
         const unsigned char* tile = smem + L.raw + st * c.stage + (tt >> 6) * t.tl.bytes;
         const bool live = tt < w.tokens(u), draft = w.draft(u);
-        const uint4 szv = *reinterpret_cast<const uint4*>(tile + t.tl.vsz + 16 * j);
-        const uint32_t sz[4] = {szv.x, szv.y, szv.z, szv.w};
+        const uint32_t* szp = reinterpret_cast<const uint32_t*>(tile + t.tl.vsz + 16 * j);
         unsigned char* row = smem + L.v + vb * kVBytes + tt * 128;
         uint32_t bits = 0u;
-#pragma unroll
+#pragma unroll 2
         for (int g = 0; g < 4; ++g) {
           // a masked drafted value that is not finite must not meet a weight of
           // zero in the product: it is left out here and added at the end
-          const bool off = draft && ((sz[g] & 0x7C00u) == 0x7C00u || (sz[g] & 0x7C000000u) == 0x7C000000u);
+          const uint32_t sz = szp[g];
+          const bool off = draft && ((sz & 0x7C00u) == 0x7C00u || (sz & 0x7C000000u) == 0x7C000000u);
           if (off) bits |= 1u << g;
-          const uint32_t use = live && !off ? sz[g] : 0u;
+          const uint32_t use = live && !off ? sz : 0u;
           const __half2 s2 = __hmul2(__half2half2(__ushort_as_half(static_cast<unsigned short>(use))), sixteenth);
           const __half2 z2 = __hmul2(__half2half2(__ushort_as_half(static_cast<unsigned short>(use >> 16))), sixteenth);
           uint32_t lo[4], hi[4];  // codes of dims (8c + k, 8c + k + 4), k = 0..3, of 8-dim chunk c: two fields 16 bits apart
@@ -575,160 +606,173 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       }
   } else if (warp < kMmaWarp) {
     // ============================================================ weights
-    const int quarter = warp & 3, half = (warp - kSWarp0) >> 2, tt = 32 * quarter + lane, stid = tid - 32 * kSWarp0;
-    const int nb = c.rb / 16;  // 16-row groups; this warp takes those of parity `half`
-    float* sc = reinterpret_cast<float*>(smem + L.rowc);
-    float* nref = sc + 128;
-    float* fac = nref + 128;
-    float* cmax = reinterpret_cast<float*>(smem + L.cmax);
-    uint64_t* mrow = reinterpret_cast<uint64_t*>(smem + L.mask);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWeights));
+    const int quarter = warp & 3, half = (warp - kSWarp0) >> 2, tt = 32 * quarter + lane, stid = tid & 127;
+    const int col0 = 16 * NBW * half;                          // this warp's rows of the block
+    const int nbw = min(NBW, c.rb / 16 - NBW * half);          // and their groups of 16
+    float4* rowc = reinterpret_cast<float4*>(smem + L.rowc) + col0 / 2;
+    float* fac = reinterpret_cast<float*>(smem + L.rowc) + 256 + col0;
+    float* cmax = reinterpret_cast<float*>(smem + L.cmax) + col0;
+    uint64_t* mrow = reinterpret_cast<uint64_t*>(smem + L.mask) + col0;
     const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + L.bad);
-    const uint32_t laddr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    const uint32_t laddr = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + static_cast<uint32_t>(col0);
     const int planes = c.rb > 64 ? 2 : 1;
+    // logits are kept in registers between the two passes when they fit beside the sums
+    constexpr bool kKeep = NBW <= 2;
+    constexpr int kHeld = kKeep ? NBW : 1;
     bool ok = true;
     int n = 0;            // units so far
     uint32_t oph = 0;
     int it = 0;
     for (bool more = any; more; more = w.next(p), ++it) {
       const int64_t item = w.bh(p) * c.nrb + w.rbk;
-      uint64_t lsum[4][8];  // sums of this token's weights, pairs of rows
+      uint64_t lsum[NBW][8];  // sums of this token's weights, pairs of rows
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < NBW; ++i)
 #pragma unroll
         for (int k = 0; k < 8; ++k) lsum[i][k] = 0ull;
-      if (stid < c.rb) {
-        const int row = w.rbk * c.rb + stid, i = row / t.G;
-        sc[stid] = p.scale[item * c.rb + stid];
-        nref[stid] = INFINITY;  // -ref of "nothing seen"
+      if (stid < 16 * nbw) {
+        const int col = col0 + stid, i = (w.rbk * c.rb + col) / t.G;
+        float* rc = reinterpret_cast<float*>(rowc) + 4 * (stid >> 1) + (stid & 1);
+        rc[0] = p.scale[item * c.rb + col];
+        rc[2] = kNothing;
         mrow[stid] = i >= w.nd ? 0ull
                      : t.mask ? t.mask[static_cast<int64_t>(w.b) * t.N + i]
                      : i == 63 ? ~0ull : (2ull << i) - 1ull;
       }
-      s_sync();
+      s_sync(half);
       for (int u = w.u0; u < w.u1; ++u, ++n) {
         const bool first_u = u == w.u0, draft = w.draft(u), live = tt < w.tokens(u);
+        const bool special = draft || w.tokens(u) < kUnit;
         if (ok) ok = bar_wait(&s_full[n & 1], (n >> 1) & 1, limit, err);
         ok = __all_sync(0xffffffffu, ok);
         fence_after();
         const uint32_t saddr = laddr + kColS + 128 * (n & 1);
+        uint32_t v[kHeld][16];
+        auto load = [&](int i, uint32_t(&x)[16]) {  // group i's logits (the caller waits)
+          ld16(x, saddr + 16 * i);
+        };
+        if (kKeep) {
+#pragma unroll
+          for (int i = 0; i < NBW; ++i)
+            if (i < nbw) load(i, v[kKeep ? i : 0]);
+          wait_ld();
+          if (special)
+#pragma unroll
+            for (int i = 0; i < NBW; ++i)
+              if (i < nbw) mask16(v[kKeep ? i : 0], 0, mrow + 16 * i, tt, live, draft);
+        }
         bool move = first_u;
         if (!first_u) {  // does any logit pass its row's ref + 15?
           float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int blk = 2 * i + half;
-            if (blk < nb) {
-              uint32_t v[16];
-              ld16(v, saddr + 16 * blk);
-              wait_ld();
+          for (int i = 0; i < NBW; ++i)
+            if (i < nbw) {
+              uint32_t(&x)[16] = v[kKeep ? i : 0];
+              if (!kKeep) {
+                load(i, x);
+                wait_ld();
+                if (special) mask16(x, 0, mrow + 16 * i, tt, live, draft);
+              }
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
-                const uint64_t s2 = *reinterpret_cast<const uint64_t*>(sc + 16 * blk + k);
-                const uint64_t r2 = *reinterpret_cast<const uint64_t*>(nref + 16 * blk + k);
-                uint64_t x;
-                asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"((static_cast<uint64_t>(v[k + 1]) << 32) | v[k]), "l"(s2), "l"(r2));
-                float a = f32x2_lo(x), b = f32x2_hi(x);
-                if (draft) {
-                  if (!((mrow[16 * blk + k] >> (tt & 63)) & 1ull)) a = -INFINITY;
-                  if (!((mrow[16 * blk + k + 1] >> (tt & 63)) & 1ull)) b = -INFINITY;
-                }
-                top = fmaxf(top, fmaxf(a, b));
+                const float4 rc = rowc[8 * i + (k >> 1)];
+                uint64_t y;
+                asm("fma.rn.f32x2 %0, %1, %2, %3;"
+                    : "=l"(y)
+                    : "l"((static_cast<uint64_t>(x[k + 1]) << 32) | x[k]), "l"(pack2(rc.x, rc.y)), "l"(pack2(rc.z, rc.w)));
+                top = fmaxf(top, fmaxf(f32x2_lo(y), f32x2_hi(y)));
               }
             }
-          }
-          move = s_any(live && top > kRefMove);
+          move = s_any(half, top > kRefMove);
         }
         if (move) {
           // column maxima of this unit
 #pragma unroll 1
-          for (int blk = half; blk < nb; blk += 2) {
-            uint32_t v[16];
-            ld16(v, saddr + 16 * blk);
+          for (int i = 0; i < nbw; ++i) {
+            uint32_t z[16];
+            load(i, z);
             wait_ld();
+            if (special) mask16(z, 0, mrow + 16 * i, tt, live, draft);
             float x[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              x[k] = __uint_as_float(v[k]) * sc[16 * blk + k];
-              if (!live || (draft && !((mrow[16 * blk + k] >> (tt & 63)) & 1ull))) x[k] = -INFINITY;
-            }
+            for (int k = 0; k < 16; ++k)
+              x[k] = __uint_as_float(z[k]) * reinterpret_cast<const float*>(rowc)[4 * (8 * i + (k >> 1)) + (k & 1)];
             int col;
             const float m = reduce16(x, lane, &col, [](float a, float b) { return fmaxf(a, b); });
-            if (!(lane & 1)) cmax[128 * quarter + 16 * blk + col] = m;
+            if (!(lane & 1)) cmax[128 * quarter + 16 * i + col] = m;
           }
-          s_sync();
-          if (stid < c.rb) {
+          s_sync(half);
+          if (stid < 16 * nbw) {
             const float m = fmaxf(fmaxf(cmax[stid], cmax[128 + stid]), fmaxf(cmax[256 + stid], cmax[384 + stid]));
-            const float old = nref[stid];                          // -ref, +inf: nothing seen
+            float* rc = reinterpret_cast<float*>(rowc) + 4 * (stid >> 1) + (stid & 1);
+            const float old = rc[2];
             const float now = m == -INFINITY ? old : fminf(old, kRefBelow - m);
-            nref[stid] = now;
+            rc[2] = now;
             fac[stid] = now == old ? 1.0f : ex2(now - old);  // 2^(old ref - new ref); nothing seen: 0
           }
-          s_sync();
+          s_sync(half);
           if (!first_u) {
             // the sums and outputs so far, relative to the new references
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int blk = 2 * i + half;
-              if (blk < nb)
+            for (int i = 0; i < NBW; ++i)
+              if (i < nbw)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                  const float2 f = *reinterpret_cast<const float2*>(fac + 16 * blk + 2 * k);
+                  const float2 f = *reinterpret_cast<const float2*>(fac + 16 * i + 2 * k);
                   lsum[i][k] = pack2(f32x2_lo(lsum[i][k]) * f.x, f32x2_hi(lsum[i][k]) * f.y);
                 }
-            }
             const int q = n - 1;  // the last product into the outputs
             if (ok) ok = bar_wait(&p_empty[q % c.np], (q / c.np) & 1, limit, err);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
 #pragma unroll 1
-            for (int blk = half; blk < nb; blk += 2) {
-              uint32_t v[16];
-              ld16(v, laddr + kColO + 16 * blk);
+            for (int i = 0; i < nbw; ++i) {
+              uint32_t z[16];
+              ld16(z, laddr + kColO + 16 * i);
               wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * fac[16 * blk + k]);
-              st16(laddr + kColO + 16 * blk, v);
+              for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(__uint_as_float(z[k]) * fac[16 * i + k]);
+              st16(laddr + kColO + 16 * i, z);
             }
             wait_st();
           }
         }
         // weights
-        const int pb = n % c.np;
+        const int pb = c.np == 2 ? n & 1 : 0;
         if (n >= c.np) {
-          if (ok) ok = bar_wait(&p_empty[pb], (n / c.np - 1) & 1, limit, err);
+          if (ok) ok = bar_wait(&p_empty[pb], c.np == 2 ? ((n >> 1) - 1) & 1 : (n - 1) & 1, limit, err);
           ok = __all_sync(0xffffffffu, ok);
         }
         unsigned char* prow = smem + L.pw + pb * planes * kPlane + tt * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int blk = 2 * i + half;
-          if (blk < nb) {
-            uint32_t v[16];
-            ld16(v, saddr + 16 * blk);
-            wait_ld();
+        for (int i = 0; i < NBW; ++i)
+          if (i < nbw) {
+            uint32_t(&x)[16] = v[kKeep ? i : 0];
+            if (!kKeep) {
+              load(i, x);
+              wait_ld();
+              if (special) mask16(x, 0, mrow + 16 * i, tt, live, draft);
+            }
             uint32_t h[8];
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              const uint64_t s2 = *reinterpret_cast<const uint64_t*>(sc + 16 * blk + k);
-              const uint64_t r2 = *reinterpret_cast<const uint64_t*>(nref + 16 * blk + k);
-              uint64_t x;
-              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"((static_cast<uint64_t>(v[k + 1]) << 32) | v[k]), "l"(s2), "l"(r2));
-              float a = ex2(f32x2_lo(x)), b = ex2(f32x2_hi(x));
-              if (!live) a = b = 0.0f;
-              if (draft) {
-                if (!((mrow[16 * blk + k] >> (tt & 63)) & 1ull)) a = 0.0f;
-                if (!((mrow[16 * blk + k + 1] >> (tt & 63)) & 1ull)) b = 0.0f;
-              }
+              const float4 rc = rowc[8 * i + (k >> 1)];
+              uint64_t y;
+              asm("fma.rn.f32x2 %0, %1, %2, %3;"
+                  : "=l"(y)
+                  : "l"((static_cast<uint64_t>(x[k + 1]) << 32) | x[k]), "l"(pack2(rc.x, rc.y)), "l"(pack2(rc.z, rc.w)));
+              const float a = ex2(f32x2_lo(y)), b = ex2(f32x2_hi(y));
               asm("add.rn.f32x2 %0, %1, %2;" : "=l"(lsum[i][k >> 1]) : "l"(lsum[i][k >> 1]), "l"(pack2(a, b)));
               const __half2 hh = __floats2half2_rn(a, b);
               h[k >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
             }
+            const int blk = NBW * half + i;
             unsigned char* dst = prow + (blk >> 2) * kPlane;
             const int c0 = 2 * (blk & 3);
             *reinterpret_cast<uint4*>(dst + (((c0 ^ tt) & 7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4*>(dst + ((((c0 + 1) ^ tt) & 7) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
           }
-        }
         fence_async_smem();
         fence_before();
         __syncwarp();
@@ -738,11 +782,10 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         }
       }
       // ---- the item's end: sums over the tokens, outputs
-      s_sync();
+      s_sync(half);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int blk = 2 * i + half;
-        if (blk < nb) {
+      for (int i = 0; i < NBW; ++i)
+        if (i < nbw) {
           float x[16];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -751,13 +794,12 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
           }
           int col;
           const float s = reduce16(x, lane, &col, [](float a, float b) { return a + b; });
-          if (!(lane & 1)) cmax[128 * quarter + 16 * blk + col] = s;
+          if (!(lane & 1)) cmax[128 * quarter + 16 * i + col] = s;
         }
-      }
       if (ok) ok = bar_wait(o_full, oph, limit, err);
       oph ^= 1u;
       ok = __all_sync(0xffffffffu, ok);
-      const bool fine = !s_any(!ok);
+      const bool fine = !s_any(half, !ok);
       fence_after();
       const bool whole = w.u0 == 0 && w.u1 == w.units;
       const bool has_draft = w.u1 == w.units;
@@ -765,60 +807,68 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       const int slot = 2 * blockIdx.x + (first < item_start ? 1 : 0);
       // tensor-memory lane -> dim: values were paired four dims apart
       const int dim = (tt & ~7) + ((tt & 7) >> 1) + 4 * (tt & 1);
+      const float nan = __int_as_float(0x7fc00000);
+      const uint32_t* badi = bad + 64 * (it % kBadRing);
+      const bool some_bad = has_draft && __any_sync(0xffffffffu, (lane < w.nd && badi[lane] != 0u) ||
+                                                                     (lane + 32 < w.nd && badi[lane + 32] != 0u));
 #pragma unroll 1
-      for (int blk = half; blk < nb; blk += 2) {
-        uint32_t v[16];
-        ld16(v, laddr + kColO + 16 * blk);
+      for (int blk = 0; blk < nbw; ++blk) {
+        uint32_t z[16];
+        ld16(z, laddr + kColO + 16 * blk);
         wait_ld();
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int col = 16 * blk + k, row = w.rbk * c.rb + col, i = row / t.G, g = row % t.G;
+          const int cc = 16 * blk + k, row = w.rbk * c.rb + col0 + cc, i = row / t.G, g = row % t.G;
           if (i >= w.nd) continue;
-          const float sum = (cmax[col] + cmax[128 + col]) + (cmax[256 + col] + cmax[384 + col]);
-          float o = __uint_as_float(v[k]) * 16.0f;
-          if (has_draft)  // drafted values that are not finite
-            for (int d = 0; d < w.nd; ++d) {
-              const uint32_t bb = bad[64 * (it % kBadRing) + d];
-              if (bb != 0u && ((bb >> (dim >> 5)) & 1u) && ((mrow[col] >> d) & 1ull)) o += __int_as_float(0x7fc00000);
-            }
-          if (!fine) o = __int_as_float(0x7fc00000);
+          const float sum = (cmax[cc] + cmax[128 + cc]) + (cmax[256 + cc] + cmax[384 + cc]);
+          float o = __uint_as_float(z[k]) * 16.0f;
+          if (some_bad)  // drafted values that are not finite
+            for (int d = 0; d < w.nd; ++d)
+              if (((badi[d] >> (dim >> 5)) & 1u) && ((mrow[cc] >> d) & 1ull)) o += nan;
+          if (!fine) o = nan;
           if (whole) {
-            const float inv = sum == 0.0f && fine ? 0.0f : 1.0f / sum;
             static_cast<__nv_bfloat16*>(t.O)[((static_cast<int64_t>(w.b) * t.N + i) * t.Hq + w.hk * t.G + g) * kHeadDim + dim] =
-                __float2bfloat16_rn(sum == 0.0f && fine ? 0.0f : o * inv);
+                __float2bfloat16_rn(sum == 0.0f && fine ? 0.0f : o * (1.0f / sum));
           } else {
-            p.part_o[(static_cast<int64_t>(slot) * c.rb + col) * kHeadDim + dim] = o;
-            if (tt == 0) p.part_ml[slot * c.rb + col] = make_float2(-nref[col], fine ? sum : __int_as_float(0x7fc00000));
+            p.part_o[(static_cast<int64_t>(slot) * c.rb + col0 + cc) * kHeadDim + dim] = o;
+            if (tt == 0)
+              p.part_ml[slot * c.rb + col0 + cc] =
+                  make_float2(-reinterpret_cast<const float*>(rowc)[4 * (cc >> 1) + 2 + (cc & 1)], fine ? sum : nan);
           }
         }
       }
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(o_empty);
-      s_sync();  // the row constants and sums may be overwritten
+      s_sync(half);  // the row constants and sums may be overwritten
     }
-  } else if (warp == kMmaWarp) {
-    // ============================================================ products
-    if (lane == 0) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == kMmaWarp) {
+      // ========================================================== products (the whole warp, converged)
       bool ok = true;
       int n = 0, ring = 0, item = 0;
       uint32_t aph = 0;
       const uint32_t sq_base = smem_u32(smem + L.sq), v_base = smem_u32(smem + L.v), p_base = smem_u32(smem + L.pw);
-      const int planes = c.rb > 64 ? 2 : 1;
+      const int p_bytes = (c.rb > 64 ? 2 : 1) * kPlane;
       const uint32_t id_s = idesc_f16(c.rb, false, 0, 0), id_o = idesc_f16(c.rb, false, 1, 1);
       const int ksteps = (t.m + t.m_out) / 16;
       const uint32_t sq_bytes = static_cast<uint32_t>(c.nk) * c.rb * 128;
       bool sq_out = false;  // a copy of the projected queries is in flight
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, err));
+      };
       auto values = [&](int q, bool first_u, bool last_u) {  // O += V^T P of unit q
-        const int pb = q % c.np, vb = q & 1;
-        ok = ok && bar_wait(&p_full[pb], (q / c.np) & 1, limit, err) && bar_wait(&v_full[vb], (q >> 1) & 1, limit, err);
-        if (ok && first_u && item > 0) ok = bar_wait(o_empty, (item - 1) & 1, limit, err);
+        const int pb = c.np == 2 ? q & 1 : 0, vb = q & 1;
+        wait(&p_full[pb], c.np == 2 ? (q >> 1) & 1 : q & 1);
+        wait(&v_full[vb], (q >> 1) & 1);
+        if (first_u && item > 0) wait(o_empty, (item - 1) & 1);
         if (!ok) return;
         fence_after();
+        const uint64_t vd = desc_mn(v_base + vb * kVBytes, kPlane), pd = desc_mn(p_base + pb * p_bytes, kPlane);
 #pragma unroll
-        for (int ks = 0; ks < kUnit / 16; ++ks)
-          mma_ss(tmem + kColO, desc_mn(v_base + vb * kVBytes + ks * 2048, kPlane),
-                 desc_mn(p_base + pb * planes * kPlane + ks * 2048, kPlane), id_o, !(first_u && ks == 0));
+        for (int ks = 0; ks < kUnit / 16; ks += 2)
+          mma_ss_mn2(tmem + kColO, vd + ks * 128, pd + ks * 128, id_o, !(first_u && ks == 0));
         commit(&p_empty[pb]);
         commit(&v_empty[vb]);
         if (last_u) commit(o_full);
@@ -826,28 +876,33 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       for (bool more = any; more && ok; more = w.next(p), ++item) {
         // the last item's score products are done: its logits were read (s_full was waited for by the weights, and
         // `values` of its last unit waited for those)
-        bar_expect(sq_full, sq_bytes);
-        bulk_load(sq_base, p.image + (w.bh(p) * c.nrb + w.rbk) * static_cast<int64_t>(sq_bytes), sq_bytes, sq_full);
+        if (lane == 0) {
+          bar_expect(sq_full, sq_bytes);
+          bulk_load(sq_base, p.image + (w.bh(p) * c.nrb + w.rbk) * static_cast<int64_t>(sq_bytes), sq_bytes, sq_full);
+        }
+        __syncwarp();
         sq_out = true;
-        ok = bar_wait(sq_full, item & 1, limit, err);
+        wait(sq_full, item & 1);
         if (!ok) break;
         sq_out = false;
         for (int u = w.u0; u < w.u1 && ok; ++u, ++n) {
-          if (n >= 2) ok = bar_wait(&s_empty[n & 1], ((n >> 1) - 1) & 1, limit, err);
-          for (int kc = 0; kc < c.nk && ok; ++kc) {
-            ok = bar_wait(&a_full[ring], aph, limit, err);
+          if (n >= 2) wait(&s_empty[n & 1], ((n >> 1) - 1) & 1);
+          uint64_t qd = desc_k(sq_base);
+          const uint32_t sd = tmem + kColS + 128 * (n & 1);
+#pragma unroll 1
+          for (int kc = 0; kc < c.nk; kc += 2, qd += c.rb * 16) {
+            wait(&a_full[ring], aph);
             if (!ok) break;
             fence_after();
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              if (4 * kc + ks < ksteps)
-                mma_ts(tmem + kColS + 128 * (n & 1), tmem + kColA + 32 * ring + 8 * ks,
-                       desc_k(sq_base + kc * c.rb * 128 + 32 * ks), id_s, kc + ks > 0);
+            const uint32_t ad = tmem + kColA + 64 * ring;
+            // (an odd number of sign words ends in half a chunk)
+            if (4 * kc + 4 <= ksteps) mma_ts_64<true>(sd, ad, qd, id_s, kc > 0);
+            else mma_ts_64<false>(sd, ad, qd, id_s, kc > 0);
+            if (4 * kc + 8 <= ksteps) mma_ts_64<true>(sd, ad + 32, qd + c.rb * 8, id_s, true);
+            else if (4 * kc + 4 < ksteps) mma_ts_64<false>(sd, ad + 32, qd + c.rb * 8, id_s, true);
             commit(&a_empty[ring]);
-            if (++ring == kARing) {
-              ring = 0;
-              aph ^= 1u;
-            }
+            ring ^= 1;
+            aph ^= ring == 0 ? 1u : 0u;
           }
           if (!ok) break;
           commit(&s_full[n & 1]);
@@ -861,16 +916,15 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       if (sq_out) bar_wait(sq_full, item & 1, limit_drain, nullptr);
     }
     __syncwarp();
-  } else {
-    // ============================================================ cache tiles
-    if (lane == 0) {
+    if (warp == kLoadWarp) {
+      // ========================================================== cache tiles (the whole warp, one lane copies)
       bool ok = true;
       int st = 0, issued = 0;
       uint32_t eph = 1;
       for (bool more = any; more && ok; more = w.next(p)) {
         const int64_t bh = w.bh(p);
         for (int u = w.u0; u < w.u1; ++u) {
-          ok = bar_wait(&raw_empty[st], eph, limit, err);
+          ok = __all_sync(0xffffffffu, bar_wait(&raw_empty[st], eph, limit, err));
           if (!ok) break;
           const unsigned char* src;
           int tiles = 1;
@@ -881,8 +935,11 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
             tiles = w.len - u * kUnit > kDecodeTileTokens ? 2 : 1;
           }
           const uint32_t bytes = static_cast<uint32_t>(tiles * t.tl.bytes);
-          bar_expect(&raw_full[st], bytes);
-          bulk_load(smem_u32(smem + L.raw + st * c.stage), src, bytes, &raw_full[st]);
+          if (lane == 0) {
+            bar_expect(&raw_full[st], bytes);
+            bulk_load(smem_u32(smem + L.raw + st * c.stage), src, bytes, &raw_full[st]);
+          }
+          __syncwarp();
           ++issued;
           if (++st == c.ns) {
             st = 0;
@@ -930,7 +987,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeTcParams p) {
   auto slot = [&](long long c) { return 2 * c + (total * c / p.grid < u0 ? 1 : 0); };
   // (with fewer units than blocks some of them have none)
   auto idle = [&](long long c) { return total * (c + 1) / p.grid == total * c / p.grid; };
-  float M = -INFINITY, L = 0.0f;
+  float M = -kNothing, L = 0.0f;
   for (long long c = c0; c <= c1; ++c)
     if (!idle(c)) M = fmaxf(M, p.part_ml[slot(c) * p.c.rb + col].x);
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -938,7 +995,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeTcParams p) {
     if (idle(c)) continue;
     const int64_t s = slot(c) * p.c.rb + col;
     const float2 ml = p.part_ml[s];
-    if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // nothing seen (a NaN sum stays)
+    if (ml.y == 0.0f) continue;  // nothing seen (a NaN sum stays)
     const float f = ml.x == M ? 1.0f : exp2f(ml.x - M);
     const float4 o = reinterpret_cast<const float4*>(p.part_o)[s * (kHeadDim / 4) + lane];
     L = fmaf(ml.y, f, L);
@@ -974,7 +1031,9 @@ cudaError_t launch_tree_attention_tc(const TreeParams& t, cudaStream_t s) {
   p.grid = static_cast<int>(most < t.num_sms ? most : t.num_sms);
   // one block per SM: it takes all tensor-memory columns
   const size_t smem = p.c.smem < 116 * 1024 ? 116 * 1024 : static_cast<size_t>(p.c.smem);
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(tree_tc_kernel), smem);
+  void (*const kernels[])(TreeTcParams) = {tree_tc_kernel<1>, tree_tc_kernel<2>, tree_tc_kernel<3>, tree_tc_kernel<4>};
+  void (*const kernel)(TreeTcParams) = kernels[(p.c.rb / 16 + 1) / 2 - 1];
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   tree_prepare_kernel<<<dim3(static_cast<unsigned>(p.c.nrb * p.c.rb / 16), static_cast<unsigned>(t.B * t.Hkv)),
                         32 * kPrepWarps, 0, s>>>(p);
@@ -990,7 +1049,7 @@ cudaError_t launch_tree_attention_tc(const TreeParams& t, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_tc_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(t.B) * t.N * t.Hq;
   cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
