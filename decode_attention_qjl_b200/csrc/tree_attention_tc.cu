@@ -13,8 +13,8 @@
 // tokens (lane = token), which keeps it out of shared memory.
 //
 // Roles of a persistent block (one per SM, all 512 tensor-memory columns):
-//   warps 0-3    signs and norms of 128 tokens -> tensor memory, 128 projections
-//                at a time (a ring of two)
+//   warps 0-3    signs and norms of 128 tokens -> tensor memory (two buffers, of
+//                all projections when they fit beside the accumulators)
 //   warps 4-7    value codes -> fp16 values in shared memory, thread = token
 //   warps 8-15   logits -> weights (fp16, shared memory), running maximum, sums
 //   warp 16      issues every tcgen05.mma
@@ -41,9 +41,7 @@ constexpr int kSWarp0 = kKWarps + kVWarps, kMmaWarp = kSWarp0 + kSWarps, kLoadWa
 constexpr int kTreeTcThreads = 640;      // five warpgroups; two warps of the last are idle
 // Registers per thread of the roles (setmaxnreg): 128 * (72 + 72 + 2 * 136 + 64) = 640 * 96, what the launch holds.
 constexpr int kRegsExpand = 72, kRegsWeights = 136, kRegsIssue = 64;
-constexpr int kARing = 2;               // sign operand chunks of 128 projections (64 columns)
 constexpr int kMaxStages = 4;
-constexpr int kColS = 0, kColO = 256, kColA = 384;  // tensor-memory columns: 2 x 128 logits, outputs, signs
 constexpr int kVBytes = kUnit * kHeadDim * 2;       // values of a unit
 constexpr int kPlane = kUnit * 128;                 // 64 rows' weights of a unit
 constexpr float kRefBelow = 4.0f, kRefMove = 15.0f;
@@ -52,14 +50,15 @@ constexpr float kNothing = 3.0e38f;                 // -ref of a row that has se
 struct TreeTcCfg {
   int rb;      // rows of a block (a multiple of 16, at most 128)
   int nrb;     // row blocks of N * G rows
-  int nk;      // 64-projection chunks
+  int nk;      // 64-projection steps
+  int ck;      // steps of a sign operand chunk (two chunks in tensor memory)
   int np;      // weight buffers
   int ns;      // cache stages
   int stage;   // bytes of a stage
   int smem;
 };
 constexpr int kBadRing = 4;  // items whose drafted values may be in flight at once (three)
-constexpr int kMiscBytes = 3 * 128 * 4 + 4 * 128 * 4 + 128 * 8 + kBadRing * 64 * 4 + 40 * 8 + 64;
+constexpr int kMiscBytes = 3 * 128 * 4 + 4 * 128 * 4 + 2 * 128 * 8 + kBadRing * 64 * 4 + 40 * 8 + 64;
 
 // Row block, buffers and stages: the largest row block (fewest passes over the
 // cache) that leaves two stages, then a second weight buffer, then stages.
@@ -87,6 +86,9 @@ TreeTcCfg tree_tc_cfg(int N, int G, int m, int m_out, int tile_bytes) {
       }
     }
     c.smem = total() + 1024;
+    // tensor memory: two logit buffers and the outputs, then the signs
+    c.ck = (512 - 3 * c.rb) / 64;
+    if (c.ck > c.nk) c.ck = c.nk;
     return c;
   }
 }
@@ -340,9 +342,9 @@ struct TreeTcSmem {
     v = c.nk * c.rb * 128;
     pw = v + 2 * kVBytes;
     raw = pw + c.np * (c.rb > 64 ? 2 : 1) * kPlane;
-    rowc = raw + c.ns * c.stage;  // float4 [64]: scales and -refs of two rows; float [128]: rescaling factor
+    rowc = raw + c.ns * c.stage;  // float4 [64]: scales and -refs of two rows; float [128]: rescaling, then output factor
     cmax = rowc + 3 * 128 * 4;    // float [4][128]: column maxima, then sums, of the lane quarters
-    mask = cmax + 4 * 128 * 4;    // uint64 [128]
+    mask = cmax + 4 * 128 * 4 + 128 * 8;  // (after int64 [128]: where a row's outputs go) uint64 [128]
     bad = mask + 128 * 8;         // uint32 [kBadRing][64]: value groups of a drafted token that are not finite
     bars = bad + kBadRing * 64 * 4;
     misc = bars + 40 * 8;
@@ -388,15 +390,6 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, int* col, Op
   return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-// Logits that do not count become -inf: dead tokens, and in the draft tile
-// what the rows' masks leave out.
-template <int N>
-__device__ __forceinline__ void mask16(uint32_t (&v)[N], int at, const uint64_t* mrow, int tt, bool live, bool draft) {
-#pragma unroll
-  for (int k = 0; k < 16; ++k)
-    if (!live || (draft && !((mrow[k] >> (tt & 63)) & 1ull))) v[at + k] = 0xFF800000u;
-}
-
 // NBW: 16-row groups of a weight warp.
 template <int NBW>
 __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid_constant__ TreeTcParams p) {
@@ -411,14 +404,11 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L.bars);
   uint64_t* raw_empty = raw_full + kMaxStages;
   uint64_t* a_full = raw_empty + kMaxStages;
-  uint64_t* a_empty = a_full + kARing;
-  uint64_t* s_full = a_empty + kARing;
-  uint64_t* s_empty = s_full + 2;
-  uint64_t* p_full = s_empty + 2;
-  uint64_t* p_empty = p_full + 2;
-  uint64_t* v_full = p_empty + 2;
-  uint64_t* v_empty = v_full + 2;
-  uint64_t* sq_full = v_empty + 2;
+  uint64_t* a_empty = a_full + 2;
+  uint64_t* s_full = a_empty + 2;
+  uint64_t* pv_full = s_full + 2;    // weights and values of a unit
+  uint64_t* pv_empty = pv_full + 2;  // their product is done
+  uint64_t* sq_full = pv_empty + 2;
   uint64_t* o_full = sq_full + 1;
   uint64_t* o_empty = o_full + 1;
   uint64_t* drain = o_empty + 1;
@@ -429,17 +419,12 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       bar_init(&raw_full[k], 1);
       bar_init(&raw_empty[k], kKWarps + kVWarps);
     }
-    for (int k = 0; k < kARing; ++k) {
+    for (int k = 0; k < 2; ++k) {
       bar_init(&a_full[k], kKWarps);
       bar_init(&a_empty[k], 1);
-    }
-    for (int k = 0; k < 2; ++k) {
       bar_init(&s_full[k], 1);
-      bar_init(&s_empty[k], kSWarps);
-      bar_init(&p_full[k], kSWarps);
-      bar_init(&p_empty[k], 1);
-      bar_init(&v_full[k], kVWarps);
-      bar_init(&v_empty[k], 1);
+      bar_init(&pv_full[k], kSWarps + kVWarps);
+      bar_init(&pv_empty[k], 1);
     }
     bar_init(sq_full, 1);
     bar_init(o_full, 1);
@@ -461,6 +446,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
   griddep_launch();
   const long long total = p.start[t.B];
   const long long first = total * blockIdx.x / p.grid, end = total * (blockIdx.x + 1) / p.grid;
+  const int col_o = 2 * c.rb, col_a = 3 * c.rb;  // tensor-memory columns: logits at 0 and rb
   const unsigned long long limit = t.wait_cycles;
   const unsigned long long limit_drain = limit > 2000000000ull ? limit : 2000000000ull;
   Walk w;
@@ -472,7 +458,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     const int tt = 32 * warp + lane, j = tt & 63;
     const int wpt = t.m / 32, wpo = t.m_out / 32, words = wpt + wpo;
     const bool even = ((wpt | wpo) & 1) == 0;  // word pairs are 8-byte aligned and of one part
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * warp) << 16) + kColA;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * warp) << 16) + col_a;
     bool ok = true;
     int st = 0, ring = 0;
     uint32_t sph = 0, rph = 1;  // phases: stage full, chunk empty (the first pass finds every chunk empty)
@@ -487,15 +473,16 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         const uint32_t* kb = reinterpret_cast<const uint32_t*>(tile + t.tl.kbits) + j * wpt;
         const uint32_t* ko = reinterpret_cast<const uint32_t*>(tile + t.tl.kbits_out) + j * wpo - wpt;
 #pragma unroll 1
-        for (int kc = 0; kc < c.nk; kc += 2) {
+        for (int k0 = 0; k0 < c.nk; k0 += c.ck) {
           ok = bar_wait(&a_empty[ring], rph, limit, err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           fence_after();
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int w0 = 2 * (kc + half), w1 = w0 + 1;
-            if (w0 >= words) continue;
+          uint32_t dst = lane_addr + 32 * c.ck * ring;
+          const int k1 = min(c.nk, k0 + c.ck);
+#pragma unroll 1
+          for (int kc = k0; kc < k1; ++kc, dst += 32) {
+            const int w0 = 2 * kc, w1 = w0 + 1;
             uint32_t x0, x1;
             if (even) {
               const uint2 x = *reinterpret_cast<const uint2*>((w0 < wpt ? kb : ko) + w0);
@@ -507,9 +494,9 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
             }
             uint32_t e[16];
             expand_word(x0, w0 < wpt ? n_in : n_out, e);
-            st16(lane_addr + 64 * ring + 32 * half, e);
+            st16(dst, e);
             expand_word(x1, w1 < wpt ? n_in : n_out, e);
-            st16(lane_addr + 64 * ring + 32 * half + 16, e);
+            st16(dst + 16, e);
           }
           wait_st();
           fence_before();
@@ -536,7 +523,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     const __half2 sixteenth = __float2half2_rn(0.0625f);
     for (bool more = any; more && ok; more = w.next(p), ++item)
       for (int u = w.u0; u < w.u1 && ok; ++u) {
-        ok = bar_wait(&raw_full[st], sph, limit, err) && bar_wait(&v_empty[vb], vph, limit, err);
+        ok = bar_wait(&raw_full[st], sph, limit, err) && bar_wait(&pv_empty[vb], vph, limit, err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const unsigned char* tile = smem + L.raw + st * c.stage + (tt >> 6) * t.tl.bytes;
@@ -594,7 +581,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          bar_arrive(&v_full[vb]);
+          bar_arrive(&pv_full[vb]);
           bar_arrive(&raw_empty[st]);
         }
         vb ^= 1;
@@ -647,42 +634,44 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         if (ok) ok = bar_wait(&s_full[n & 1], (n >> 1) & 1, limit, err);
         ok = __all_sync(0xffffffffu, ok);
         fence_after();
-        const uint32_t saddr = laddr + kColS + 128 * (n & 1);
-        uint32_t v[kHeld][16];
-        auto load = [&](int i, uint32_t(&x)[16]) {  // group i's logits (the caller waits)
-          ld16(x, saddr + 16 * i);
-        };
-        if (kKeep) {
+        const uint32_t saddr = laddr + c.rb * (n & 1);
+        if (special) {  // logits that do not count become -inf
+#pragma unroll 1
+          for (int i = 0; i < nbw; ++i) {
+            uint32_t z[16];
+            ld16(z, saddr + 16 * i);
+            wait_ld();
 #pragma unroll
-          for (int i = 0; i < NBW; ++i)
-            if (i < nbw) load(i, v[kKeep ? i : 0]);
-          wait_ld();
-          if (special)
-#pragma unroll
-            for (int i = 0; i < NBW; ++i)
-              if (i < nbw) mask16(v[kKeep ? i : 0], 0, mrow + 16 * i, tt, live, draft);
+            for (int k = 0; k < 16; ++k)
+              if (!live || (draft && !((mrow[16 * i + k] >> (tt & 63)) & 1ull))) z[k] = 0xFF800000u;
+            st16(saddr + 16 * i, z);
+          }
+          wait_st();
         }
+        // x - ref of group i's rows, kept in registers for the weights when they fit beside the sums
+        uint64_t y[kHeld][8];
+        auto relative = [&](int i, uint64_t(&out)[8]) {
+          uint32_t z[16];
+          ld16(z, saddr + 16 * i);
+          wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 rc = rowc[8 * i + k];
+            asm("fma.rn.f32x2 %0, %1, %2, %3;"
+                : "=l"(out[k])
+                : "l"((static_cast<uint64_t>(z[2 * k + 1]) << 32) | z[2 * k]), "l"(pack2(rc.x, rc.y)), "l"(pack2(rc.z, rc.w)));
+          }
+        };
         bool move = first_u;
         if (!first_u) {  // does any logit pass its row's ref + 15?
           float top = -INFINITY;
 #pragma unroll
           for (int i = 0; i < NBW; ++i)
             if (i < nbw) {
-              uint32_t(&x)[16] = v[kKeep ? i : 0];
-              if (!kKeep) {
-                load(i, x);
-                wait_ld();
-                if (special) mask16(x, 0, mrow + 16 * i, tt, live, draft);
-              }
+              uint64_t(&x)[8] = y[kKeep ? i : 0];
+              relative(i, x);
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const float4 rc = rowc[8 * i + (k >> 1)];
-                uint64_t y;
-                asm("fma.rn.f32x2 %0, %1, %2, %3;"
-                    : "=l"(y)
-                    : "l"((static_cast<uint64_t>(x[k + 1]) << 32) | x[k]), "l"(pack2(rc.x, rc.y)), "l"(pack2(rc.z, rc.w)));
-                top = fmaxf(top, fmaxf(f32x2_lo(y), f32x2_hi(y)));
-              }
+              for (int k = 0; k < 8; ++k) top = fmaxf(top, fmaxf(f32x2_lo(x[k]), f32x2_hi(x[k])));
             }
           move = s_any(half, top > kRefMove);
         }
@@ -691,9 +680,8 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
 #pragma unroll 1
           for (int i = 0; i < nbw; ++i) {
             uint32_t z[16];
-            load(i, z);
+            ld16(z, saddr + 16 * i);
             wait_ld();
-            if (special) mask16(z, 0, mrow + 16 * i, tt, live, draft);
             float x[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -723,49 +711,44 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
                   lsum[i][k] = pack2(f32x2_lo(lsum[i][k]) * f.x, f32x2_hi(lsum[i][k]) * f.y);
                 }
             const int q = n - 1;  // the last product into the outputs
-            if (ok) ok = bar_wait(&p_empty[q % c.np], (q / c.np) & 1, limit, err);
+            if (ok) ok = bar_wait(&pv_empty[q & 1], (q >> 1) & 1, limit, err);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
 #pragma unroll 1
             for (int i = 0; i < nbw; ++i) {
               uint32_t z[16];
-              ld16(z, laddr + kColO + 16 * i);
+              ld16(z, laddr + col_o + 16 * i);
               wait_ld();
 #pragma unroll
               for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(__uint_as_float(z[k]) * fac[16 * i + k]);
-              st16(laddr + kColO + 16 * i, z);
+              st16(laddr + col_o + 16 * i, z);
             }
             wait_st();
           }
+          if (kKeep)
+#pragma unroll
+            for (int i = 0; i < NBW; ++i)
+              if (i < nbw) relative(i, y[kKeep ? i : 0]);
         }
         // weights
-        const int pb = c.np == 2 ? n & 1 : 0;
-        if (n >= c.np) {
-          if (ok) ok = bar_wait(&p_empty[pb], c.np == 2 ? ((n >> 1) - 1) & 1 : (n - 1) & 1, limit, err);
+        const int pb = c.np == 2 ? n & 1 : 0, q = n - c.np;  // the buffer, and the unit whose product frees it
+        if (q >= 0) {
+          if (ok) ok = bar_wait(&pv_empty[q & 1], (q >> 1) & 1, limit, err);
           ok = __all_sync(0xffffffffu, ok);
         }
         unsigned char* prow = smem + L.pw + pb * planes * kPlane + tt * 128;
 #pragma unroll
         for (int i = 0; i < NBW; ++i)
           if (i < nbw) {
-            uint32_t(&x)[16] = v[kKeep ? i : 0];
-            if (!kKeep) {
-              load(i, x);
-              wait_ld();
-              if (special) mask16(x, 0, mrow + 16 * i, tt, live, draft);
-            }
+            uint64_t(&x)[8] = y[kKeep ? i : 0];
+            if (!kKeep) relative(i, x);
             uint32_t h[8];
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float4 rc = rowc[8 * i + (k >> 1)];
-              uint64_t y;
-              asm("fma.rn.f32x2 %0, %1, %2, %3;"
-                  : "=l"(y)
-                  : "l"((static_cast<uint64_t>(x[k + 1]) << 32) | x[k]), "l"(pack2(rc.x, rc.y)), "l"(pack2(rc.z, rc.w)));
-              const float a = ex2(f32x2_lo(y)), b = ex2(f32x2_hi(y));
-              asm("add.rn.f32x2 %0, %1, %2;" : "=l"(lsum[i][k >> 1]) : "l"(lsum[i][k >> 1]), "l"(pack2(a, b)));
+            for (int k = 0; k < 8; ++k) {
+              const float a = ex2(f32x2_lo(x[k])), b = ex2(f32x2_hi(x[k]));
+              asm("add.rn.f32x2 %0, %1, %2;" : "=l"(lsum[i][k]) : "l"(lsum[i][k]), "l"(pack2(a, b)));
               const __half2 hh = __floats2half2_rn(a, b);
-              h[k >> 1] = *reinterpret_cast<const uint32_t*>(&hh);
+              h[k] = *reinterpret_cast<const uint32_t*>(&hh);
             }
             const int blk = NBW * half + i;
             unsigned char* dst = prow + (blk >> 2) * kPlane;
@@ -776,10 +759,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         fence_async_smem();
         fence_before();
         __syncwarp();
-        if (lane == 0) {
-          bar_arrive(&s_empty[n & 1]);
-          bar_arrive(&p_full[pb]);
-        }
+        if (lane == 0) bar_arrive(&pv_full[n & 1]);  // (the logits are read, too)
       }
       // ---- the item's end: sums over the tokens, outputs
       s_sync(half);
@@ -805,36 +785,49 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       const bool has_draft = w.u1 == w.units;
       const long long item_start = first + ((end - first) - w.left) - w.u0;  // first unit of the item
       const int slot = 2 * blockIdx.x + (first < item_start ? 1 : 0);
-      // tensor-memory lane -> dim: values were paired four dims apart
-      const int dim = (tt & ~7) + ((tt & 7) >> 1) + 4 * (tt & 1);
       const float nan = __int_as_float(0x7fc00000);
+      // per row: where its dims go (-1: a row past the drafts) and the factor of its outputs
+      long long* dest = reinterpret_cast<long long*>(cmax + 512 - col0) + col0;
+      if (stid < 16 * nbw) {
+        const int col = col0 + stid, row = w.rbk * c.rb + col, i = row / t.G, g = row - i * t.G;
+        const float sum = (cmax[stid] + cmax[128 + stid]) + (cmax[256 + stid] + cmax[384 + stid]);
+        if (whole) {
+          dest[stid] = ((static_cast<long long>(w.b) * t.N + i) * t.Hq + w.hk * t.G + g) * kHeadDim;
+          fac[stid] = !fine ? nan : sum == 0.0f ? 0.0f : 16.0f / sum;
+        } else {
+          dest[stid] = (static_cast<long long>(slot) * c.rb + col) * kHeadDim;
+          fac[stid] = fine ? 16.0f : nan;
+          p.part_ml[slot * c.rb + col] =
+              make_float2(-reinterpret_cast<const float*>(rowc)[4 * (stid >> 1) + 2 + (stid & 1)], fine ? sum : nan);
+        }
+        if (i >= w.nd) dest[stid] = -1;
+      }
       const uint32_t* badi = bad + 64 * (it % kBadRing);
       const bool some_bad = has_draft && __any_sync(0xffffffffu, (lane < w.nd && badi[lane] != 0u) ||
                                                                      (lane + 32 < w.nd && badi[lane + 32] != 0u));
+      s_sync(half);
+      // tensor-memory lane -> dim: values were paired four dims apart
+      const int dim = (tt & ~7) + ((tt & 7) >> 1) + 4 * (tt & 1);
 #pragma unroll 1
       for (int blk = 0; blk < nbw; ++blk) {
         uint32_t z[16];
-        ld16(z, laddr + kColO + 16 * blk);
+        ld16(z, laddr + col_o + 16 * blk);
         wait_ld();
+        if (some_bad) {  // drafted values that are not finite
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            bool hit = false;
+            for (int d = 0; d < w.nd; ++d) hit |= ((badi[d] >> (dim >> 5)) & 1u) && ((mrow[16 * blk + k] >> d) & 1ull);
+            if (hit) z[k] = 0x7fc00000u;
+          }
+        }
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int cc = 16 * blk + k, row = w.rbk * c.rb + col0 + cc, i = row / t.G, g = row % t.G;
-          if (i >= w.nd) continue;
-          const float sum = (cmax[cc] + cmax[128 + cc]) + (cmax[256 + cc] + cmax[384 + cc]);
-          float o = __uint_as_float(z[k]) * 16.0f;
-          if (some_bad)  // drafted values that are not finite
-            for (int d = 0; d < w.nd; ++d)
-              if (((badi[d] >> (dim >> 5)) & 1u) && ((mrow[cc] >> d) & 1ull)) o += nan;
-          if (!fine) o = nan;
-          if (whole) {
-            static_cast<__nv_bfloat16*>(t.O)[((static_cast<int64_t>(w.b) * t.N + i) * t.Hq + w.hk * t.G + g) * kHeadDim + dim] =
-                __float2bfloat16_rn(sum == 0.0f && fine ? 0.0f : o * (1.0f / sum));
-          } else {
-            p.part_o[(static_cast<int64_t>(slot) * c.rb + col0 + cc) * kHeadDim + dim] = o;
-            if (tt == 0)
-              p.part_ml[slot * c.rb + col0 + cc] =
-                  make_float2(-reinterpret_cast<const float*>(rowc)[4 * (cc >> 1) + 2 + (cc & 1)], fine ? sum : nan);
-          }
+          const long long to = dest[16 * blk + k];
+          const float f = fac[16 * blk + k], o = f == 0.0f ? 0.0f : __uint_as_float(z[k]) * f;
+          if (to < 0) continue;
+          if (whole) static_cast<__nv_bfloat16*>(t.O)[to + dim] = __float2bfloat16_rn(o);
+          else p.part_o[to + dim] = o;
         }
       }
       fence_before();
@@ -852,7 +845,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       const uint32_t sq_base = smem_u32(smem + L.sq), v_base = smem_u32(smem + L.v), p_base = smem_u32(smem + L.pw);
       const int p_bytes = (c.rb > 64 ? 2 : 1) * kPlane;
       const uint32_t id_s = idesc_f16(c.rb, false, 0, 0), id_o = idesc_f16(c.rb, false, 1, 1);
-      const int ksteps = (t.m + t.m_out) / 16;
+      const bool half_step = ((t.m + t.m_out) & 32) != 0;  // an odd number of sign words ends in half a step
       const uint32_t sq_bytes = static_cast<uint32_t>(c.nk) * c.rb * 128;
       bool sq_out = false;  // a copy of the projected queries is in flight
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -860,17 +853,15 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       };
       auto values = [&](int q, bool first_u, bool last_u) {  // O += V^T P of unit q
         const int pb = c.np == 2 ? q & 1 : 0, vb = q & 1;
-        wait(&p_full[pb], c.np == 2 ? (q >> 1) & 1 : q & 1);
-        wait(&v_full[vb], (q >> 1) & 1);
+        wait(&pv_full[vb], (q >> 1) & 1);
         if (first_u && item > 0) wait(o_empty, (item - 1) & 1);
         if (!ok) return;
         fence_after();
         const uint64_t vd = desc_mn(v_base + vb * kVBytes, kPlane), pd = desc_mn(p_base + pb * p_bytes, kPlane);
 #pragma unroll
         for (int ks = 0; ks < kUnit / 16; ks += 2)
-          mma_ss_mn2(tmem + kColO, vd + ks * 128, pd + ks * 128, id_o, !(first_u && ks == 0));
-        commit(&p_empty[pb]);
-        commit(&v_empty[vb]);
+          mma_ss_mn2(tmem + col_o, vd + ks * 128, pd + ks * 128, id_o, !(first_u && ks == 0));
+        commit(&pv_empty[vb]);
         if (last_u) commit(o_full);
       };
       for (bool more = any; more && ok; more = w.next(p), ++item) {
@@ -886,20 +877,19 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         if (!ok) break;
         sq_out = false;
         for (int u = w.u0; u < w.u1 && ok; ++u, ++n) {
-          if (n >= 2) wait(&s_empty[n & 1], ((n >> 1) - 1) & 1);
+          // (the logits of unit n - 2 in this buffer were read before its weights, which `values` waited for)
           uint64_t qd = desc_k(sq_base);
-          const uint32_t sd = tmem + kColS + 128 * (n & 1);
+          const uint32_t sd = tmem + c.rb * (n & 1);
 #pragma unroll 1
-          for (int kc = 0; kc < c.nk; kc += 2, qd += c.rb * 16) {
+          for (int k0 = 0; k0 < c.nk; k0 += c.ck) {
             wait(&a_full[ring], aph);
             if (!ok) break;
             fence_after();
-            const uint32_t ad = tmem + kColA + 64 * ring;
-            // (an odd number of sign words ends in half a chunk)
-            if (4 * kc + 4 <= ksteps) mma_ts_64<true>(sd, ad, qd, id_s, kc > 0);
-            else mma_ts_64<false>(sd, ad, qd, id_s, kc > 0);
-            if (4 * kc + 8 <= ksteps) mma_ts_64<true>(sd, ad + 32, qd + c.rb * 8, id_s, true);
-            else if (4 * kc + 4 < ksteps) mma_ts_64<false>(sd, ad + 32, qd + c.rb * 8, id_s, true);
+            uint32_t ad = tmem + col_a + 32 * c.ck * ring;
+            const int k1 = min(c.nk, k0 + c.ck), full = k1 == c.nk && half_step ? k1 - 1 : k1;
+#pragma unroll 1
+            for (int kc = k0; kc < full; ++kc, ad += 32, qd += c.rb * 8) mma_ts_64<true>(sd, ad, qd, id_s, kc > 0);
+            if (full < k1) mma_ts_64<false>(sd, ad, qd, id_s, full > 0);
             commit(&a_empty[ring]);
             ring ^= 1;
             aph ^= ring == 0 ? 1u : 0u;
