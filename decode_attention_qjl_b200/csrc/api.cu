@@ -677,6 +677,7 @@ qjl_status qjl_cache_read(qjl_ctx* ctx, const qjl_cache* cache, int T, const int
   p.v_sh = v_sh;
   p.v_st = v_st;
   p.num_sms = ctx->num_sms;
+  p.wait_cycles = wait_cycles(ctx);
   const cudaError_t e = qjl::launch_cache_read(p, dtype, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "qjl_cache_read");
   return QJL_OK;

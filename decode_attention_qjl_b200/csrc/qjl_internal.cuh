@@ -302,6 +302,7 @@ struct ReadParams {
   void *K, *V;                     // outputs, either may be null
   int64_t k_sb, k_sh, k_st, v_sb, v_sh, v_st;
   int num_sms;
+  unsigned long long wait_cycles;
 };
 
 struct CommitParams {

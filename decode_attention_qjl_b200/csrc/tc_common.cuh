@@ -142,6 +142,18 @@ __device__ __forceinline__ void mma_ts_64(uint32_t d, uint32_t a, uint64_t b, ui
         "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
         : "memory");
 }
+// Products of 32 K values: A from tensor memory, B MN-major in shared memory.
+__device__ __forceinline__ void mma_ts_mn_32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, 128;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
 // Two products of 16 K values each with both operands MN-major in shared
 // memory (2048 bytes, 128 descriptor units, per 16).
 __device__ __forceinline__ void mma_ss_mn2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
