@@ -74,7 +74,10 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// 16 or 32 consecutive columns of this warp's 32 tensor-memory lanes, without the wait.
+// 1 or 16 consecutive columns of this warp's 32 tensor-memory lanes, without the wait.
+__device__ __forceinline__ void ld1(uint32_t& v, uint32_t taddr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr) : "memory");
+}
 __device__ __forceinline__ void ld16(uint32_t (&v)[16], uint32_t taddr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
