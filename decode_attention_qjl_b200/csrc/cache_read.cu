@@ -12,10 +12,11 @@
 // products take 1300 of the 3500 SM cycles that this costs per 128 tokens. One
 // block per SM, S and S_out in shared memory once (a K row per projection, 128
 // channels, MN-major with 128-byte swizzle), and the roles
-//   warps 0-3   sign words (global) -> tensor memory, lane = token
-//   warps 4-11  value codes (global) -> V_out, thread = half a token
-//   warps 12-19 sums (tensor memory) -> K_out, lane = token, half of its channels
-//   warp 20     issues the products
+//   warps 0-7   sign words (global) -> tensor memory, lane = token, every other
+//               pair of its words
+//   warps 8-15  value codes (global) -> V_out, thread = half a token
+//   warps 16-23 sums (tensor memory) -> K_out, lane = token, half of its channels
+//   warp 24     issues the products
 // Units of 128 token slots are dealt round robin. The output warps own a token
 // per lane; 32 rows written by 32 lanes, a sector each, took 3.8 SM cycles per
 // sector (208 us for 1 M token-heads, bf16), so they turn a piece of their rows
@@ -28,7 +29,7 @@ namespace {
 using namespace tc;
 
 constexpr int kReadUnit = 128;
-constexpr int kReadThreads = 32 * 21;
+constexpr int kReadThreads = 32 * 25;
 constexpr int kReadWords = 4;                // sign words of a chunk: 64 tensor-memory columns
 constexpr int kReadColOut = 256, kReadColA = 384;  // two D_in at 0 and 128, D_out, two sign chunks
 constexpr int kReadMisc = 1024;
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kReadThreads, 1) cache_read_kernel(const __gri
   unsigned char* stage = img + (p.K ? rows * kHeadDim * 2 : 0);  // 16 warps' row pieces
   if (tid == 0) {
     for (int k = 0; k < 2; ++k) {
-      bar_init(&a_full[k], 4);
+      bar_init(&a_full[k], 8);
       bar_init(&a_empty[k], 1);
       bar_init(&d_full[k], 1);
       bar_init(&d_empty[k], 8);
@@ -211,36 +212,37 @@ __global__ void __launch_bounds__(kReadThreads, 1) cache_read_kernel(const __gri
   const unsigned long long limit = p.wait_cycles;
   ReadUnit u;
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ============================================================ signs
-    const int tt = 32 * warp + lane;
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * warp) << 16) + kReadColA;
+    const int tt = 32 * (warp & 3) + lane, part = warp >> 2;  // words 2 part, 2 part + 1 of a chunk
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kReadColA + 32 * part;
     bool ok = p.K != nullptr;
     int ring = 0;
     uint32_t ph = 1;
     // the words of chunk w0 of unit u, fetched one chunk ahead of their use
     const uint32_t* kb = nullptr;  // this token's words (null: outside the range)
     const uint32_t* ko = nullptr;
-    const bool quads = (wpt & 3) == 0;
+    const bool pairs = ((wpt | wpo) & 1) == 0;  // word pairs are of one part and 8-byte aligned
     auto token = [&] {
       const unsigned char* tile = u.tile(p, tt);
       kb = u.live(tt) ? reinterpret_cast<const uint32_t*>(tile + p.tl.kbits) + (tt & 63) * wpt : nullptr;
       ko = reinterpret_cast<const uint32_t*>(tile + p.tl.kbits_out) + (tt & 63) * wpo - wpt;
     };
-    auto fetch = [&](int w0, uint32_t(&x)[kReadWords]) {
-      if (quads && w0 < wpt) {
-        const uint4 v = kb ? __ldg(reinterpret_cast<const uint4*>(kb + w0)) : make_uint4(0u, 0u, 0u, 0u);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    auto fetch = [&](int w0, uint32_t(&x)[2]) {
+      const int w = w0 + 2 * part;
+      x[0] = x[1] = 0u;
+      if (!kb || w >= words) return;
+      if (pairs) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>((w < wpt ? kb : ko) + w));
+        x[0] = v.x;
+        x[1] = v.y;
       } else {
-#pragma unroll
-        for (int k = 0; k < kReadWords; ++k) {
-          const int w = w0 + k;
-          x[k] = !kb || w >= words ? 0u : __ldg((w < wpt ? kb : ko) + w);
-        }
+        x[0] = __ldg((w < wpt ? kb : ko) + w);
+        if (w + 1 < words) x[1] = __ldg((w + 1 < wpt ? kb : ko) + w + 1);
       }
     };
     bool more = p.K && u.begin(p, upb, n_units);
-    uint32_t x[kReadWords];
+    uint32_t x[2];
     if (more) {
       token();
       fetch(0, x);
@@ -253,14 +255,14 @@ __global__ void __launch_bounds__(kReadThreads, 1) cache_read_kernel(const __gri
         more = u.next(p, upb, n_units);
         if (more) token();
       }
-      uint32_t y[kReadWords];
+      uint32_t y[2];
       if (more) fetch(w0, y);
       ok = __all_sync(0xffffffffu, bar_wait(&a_empty[ring], ph, limit, err));
       if (!ok) break;
       fence_after();
 #pragma unroll
-      for (int k = 0; k < kReadWords; ++k)
-        if (here + k < words) {
+      for (int k = 0; k < 2; ++k)
+        if (here + 2 * part + k < words) {
           uint32_t e[16];
           expand_word(x[k], 0x3F803F80u, e);
           st16(lane_addr + 64 * ring + 16 * k, e);
@@ -271,13 +273,13 @@ __global__ void __launch_bounds__(kReadThreads, 1) cache_read_kernel(const __gri
       if (lane == 0) bar_arrive(&a_full[ring]);
       ring ^= 1;
       ph ^= ring == 0 ? 1u : 0u;
-#pragma unroll
-      for (int k = 0; k < kReadWords; ++k) x[k] = y[k];
+      x[0] = y[0];
+      x[1] = y[1];
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ============================================================ values
-    const int tt = 32 * (warp & 3) + lane, part = (warp - 4) >> 2;  // dims 64 part ..
-RowStage<T, SEG> out{stage + 32 * SEG * (warp - 4), 0u, nullptr, p.v_st};
+    const int tt = 32 * (warp & 3) + lane, part = (warp - 8) >> 2;  // dims 64 part ..
+RowStage<T, SEG> out{stage + 32 * SEG * (warp - 8), 0u, nullptr, p.v_st};
     struct Codes {  // of this thread's half token, fetched one unit ahead of their use
       uint2 sz;
       uint4 cw[2];
@@ -336,11 +338,11 @@ RowStage<T, SEG> out{stage + 32 * SEG * (warp - 4), 0u, nullptr, p.v_st};
         }
       }
     }
-  } else if (warp < 20) {
+  } else if (warp < 24) {
     // ============================================================ keys
-    const int quarter = warp & 3, tt = 32 * quarter + lane, part = (warp - 12) >> 2;  // channels 64 part ..
+    const int quarter = warp & 3, tt = 32 * quarter + lane, part = (warp - 16) >> 2;  // channels 64 part ..
     const uint32_t laddr = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    RowStage<T, SEG> out{stage + 32 * SEG * (warp - 4), 0u, nullptr, p.k_st};
+    RowStage<T, SEG> out{stage + 32 * SEG * (warp - 8), 0u, nullptr, p.k_st};
     const float c_in = kSqrtHalfPi / static_cast<float>(p.m), c_out = p.m_out ? kSqrtHalfPi / static_cast<float>(p.m_out) : 0.0f;
     bool ok = true;
     int units = 0;
