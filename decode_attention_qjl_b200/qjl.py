@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -123,7 +124,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "qjl_exact_decode": (i32, [i32, vp, vp, ctypes.c_float, ctypes.c_float, i32, i32, i32, i32, i32, vp, i32, vp,
                                    ctypes.c_float, vp, vp, sz, vp]),
         "qjl_rope_init": (i32, [i32, f64, i32, f64, f64, f64, f64, f64, ctypes.POINTER(qjl_rope_table)]),
-        "qjl_rope": (i32, [ctypes.POINTER(qjl_rope_table), ctypes.POINTER(qjl_rope_heads), i32, i32, i32, i32, vp, vp,
+        "qjl_rope": (i32, [ctypes.POINTER(qjl_rope_table), vp, i32, i32, i32, i32, vp, vp,
                            i32, vp]),
         "qjl_cache_read": (i32, [vp, cachep, i32, vp, vp, vp, i64, i64, i64, vp, i64, i64, i64, i32, vp]),
         "qjl_tree_attention_workspace_bytes": (sz, [vp, i32, i32, i32, i32]),
@@ -447,30 +448,37 @@ def qjl_exact_decode(K, V, Q, O, T: int | None = None, seqlens=None, sm_scale: f
     return O
 
 
-def _device_tensors(fn: str, *tensors):
-    """The tensors must lie on the current CUDA device, where the call runs."""
+# The speculative step's calls are short (a few microseconds on the device), so their wrappers pass plain
+# integers, read each tensor's metadata once and take the raw stream handle.
+
+def _current(fn: str, stream, *tensors):
+    """The stream handle of a call; its tensors must lie on the current CUDA device, where it runs."""
     import torch
 
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (t.device.type != "cuda" or t.device.index != cur):
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"{fn}: tensor on {t.device}, the call runs on cuda:{cur}")
+    return torch.cuda.current_stream(cur).cuda_stream if stream is None else stream.cuda_stream
 
 
-def _index_tensor(fn: str, name: str, t, shape, dtype):
-    """An optional index argument: contiguous, of the given shape and dtype."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()):
+def _index_ptr(fn: str, name: str, t, shape, dtype):
+    """Address of an optional index argument: contiguous, of the given shape and dtype."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
-    return t
+    return t.data_ptr()
 
 
 def _head_rows(fn: str, name: str, t, shape, dtype):
-    """A tensor of head rows: the given shape and dtype, last dim contiguous."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.stride(-1) != 1):
+    """Strides of a tensor of head rows: the given shape and dtype, last dim contiguous."""
+    st = t.stride()
+    if t.shape != shape or t.dtype is not dtype or st[-1] != 1:
         raise ValueError(f"{fn}: {name} must be {dtype} {tuple(shape)} with a contiguous last dim, "
                          f"got {t.dtype} {tuple(t.shape)}")
-    return t
+    return st
 
 
 def qjl_rope_init(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0,
@@ -485,6 +493,9 @@ def qjl_rope_init(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: b
     return table
 
 
+_pack_heads = struct.Struct("@PPi6q").pack  # a qjl_rope_heads
+
+
 def qjl_rope(table: qjl_rope_table, Q, K=None, positions=None, t_start=None, Q_out=None, K_out=None,
              inverse: bool = False, stream=None):
     """Rotary positions of Q [B, Hq, T, d] and, in the same launch, K [B, Hkv, T, d] (device, bf16 or fp32, last dim
@@ -493,24 +504,27 @@ def qjl_rope(table: qjl_rope_table, Q, K=None, positions=None, t_start=None, Q_o
     inverse: rotate back, which is also the gradient. Returns Q_out, or (Q_out, K_out) when K is given."""
     import torch
 
-    pairs = [(Q, Q_out)] + ([(K, K_out)] if K is not None else [])
-    B, _, T, d = Q.shape
-    arr = (qjl_rope_heads * 2)()
-    outs = []
-    for n, (x, y) in enumerate(pairs):
-        if x.dim() != 4 or x.shape[0] != B or x.shape[2] != T or x.shape[3] != HEAD_DIM:
+    fn = "qjl_rope"
+    B, _, T, _ = Q.shape
+    heads, outs = b"", []
+    for x, y in ((Q, Q_out), (K, K_out)):
+        if x is None:
+            break
+        shape = x.shape
+        if len(shape) != 4 or shape[0] != B or shape[2] != T or shape[3] != HEAD_DIM:
             raise ValueError(f"qjl_rope: tensors must be [B, H, T, {HEAD_DIM}] with one B and T")
-        y = torch.empty_like(x) if y is None else y
-        _head_rows("qjl_rope", "an input", x, x.shape, Q.dtype)
-        _head_rows("qjl_rope", "an output", y, x.shape, Q.dtype)
-        arr[n] = qjl_rope_heads(x.data_ptr(), y.data_ptr(), x.shape[1], *x.stride()[:3], *y.stride()[:3])
+        if y is None:
+            y = torch.empty_like(x)
+        a, c = _head_rows(fn, "an input", x, shape, Q.dtype), _head_rows(fn, "an output", y, shape, Q.dtype)
+        heads += _pack_heads(x.data_ptr(), y.data_ptr(), shape[1], a[0], a[1], a[2], c[0], c[1], c[2])
         outs.append(y)
-    _index_tensor("qjl_rope", "positions", positions, (B, T), torch.int32)
-    _index_tensor("qjl_rope", "t_start", t_start, (B,), torch.int32)
-    _device_tensors("qjl_rope", Q, K, positions, t_start, *outs)
-    _check("qjl_rope", load_library().qjl_rope(ctypes.byref(table), arr, len(pairs), _dtype_code(Q), B, T,
-                                               _ptr(positions), _ptr(t_start), int(inverse), _stream(stream)))
-    return outs[0] if K is None else tuple(outs)
+    pos = _index_ptr(fn, "positions", positions, (B, T), torch.int32)
+    start = _index_ptr(fn, "t_start", t_start, (B,), torch.int32)
+    cur = _current(fn, stream, Q, K, positions, t_start, *outs)
+    st = load_library().qjl_rope(table, heads, len(outs), _dtype_code(Q), B, T, pos, start, bool(inverse), cur)
+    if st:
+        _check(fn, st)
+    return outs[0] if K is None else (outs[0], outs[1])
 
 
 def qjl_cache_read(ctx, cache: QJLCache, T: int, K_out=None, V_out=None, t_start=None, seqlens=None, stream=None):
@@ -518,19 +532,21 @@ def qjl_cache_read(ctx, cache: QJLCache, T: int, K_out=None, V_out=None, t_start
     seqlens[b] (the capacity); other rows stay as they were. K_out, V_out: device bf16 or fp32 (one dtype)."""
     import torch
 
+    fn = "qjl_cache_read"
     out = K_out if K_out is not None else V_out
     if out is None:
         raise ValueError("qjl_cache_read: K_out and V_out are both missing")
-    strides = []
-    for name, t in (("K_out", K_out), ("V_out", V_out)):
-        _head_rows("qjl_cache_read", name, t, (cache.B, cache.Hkv, T, HEAD_DIM), out.dtype)
-        strides.append((0, 0, 0) if t is None else t.stride()[:3])
-    _index_tensor("qjl_cache_read", "t_start", t_start, (cache.B,), torch.int32)
-    _index_tensor("qjl_cache_read", "seqlens", seqlens, (cache.B,), torch.int32)
-    _device_tensors("qjl_cache_read", K_out, V_out, t_start, seqlens, cache.tiles)
-    st = load_library().qjl_cache_read(ctx, ctypes.byref(cache.struct()), T, _ptr(t_start), _ptr(seqlens), _ptr(K_out),
-                                       *strides[0], _ptr(V_out), *strides[1], _dtype_code(out), _stream(stream))
-    _check("qjl_cache_read", st)
+    shape = (cache.B, cache.Hkv, T, HEAD_DIM)
+    k = (0, 0, 0) if K_out is None else _head_rows(fn, "K_out", K_out, shape, out.dtype)
+    v = (0, 0, 0) if V_out is None else _head_rows(fn, "V_out", V_out, shape, out.dtype)
+    start = _index_ptr(fn, "t_start", t_start, (cache.B,), torch.int32)
+    lens = _index_ptr(fn, "seqlens", seqlens, (cache.B,), torch.int32)
+    cur = _current(fn, stream, K_out, V_out, t_start, seqlens, cache.tiles)
+    st = load_library().qjl_cache_read(ctx, cache.struct(), T, start, lens, None if K_out is None else K_out.data_ptr(),
+                                       k[0], k[1], k[2], None if V_out is None else V_out.data_ptr(), v[0], v[1],
+                                       v[2], _dtype_code(out), cur)
+    if st:
+        _check(fn, st)
     return K_out, V_out
 
 
@@ -546,23 +562,25 @@ def qjl_tree_attention(ctx, cache: QJLCache, draft: QJLCache, Q, T: int, O, seql
     sequence (None: N). O: device [B, N, Hq, d] of Q's dtype, contiguous, written."""
     import torch
 
-    B, N, Hq, d = Q.shape
-    if B != cache.B or d != HEAD_DIM:
+    fn = "qjl_tree_attention"
+    shape = Q.shape
+    if len(shape) != 4 or shape[0] != cache.B or shape[3] != HEAD_DIM:
         raise ValueError(f"qjl_tree_attention: Q must be [{cache.B}, N, Hq, {HEAD_DIM}]")
-    _head_rows("qjl_tree_attention", "Q", Q, Q.shape, Q.dtype)
-    _head_rows("qjl_tree_attention", "O", O, Q.shape, Q.dtype)
+    B, N, Hq, _ = shape
+    q = _head_rows(fn, "Q", Q, shape, Q.dtype)
+    _head_rows(fn, "O", O, shape, Q.dtype)
     if not O.is_contiguous():
         raise ValueError("qjl_tree_attention: O must be contiguous")
-    _index_tensor("qjl_tree_attention", "seqlens", seqlens, (B,), torch.int32)
-    _index_tensor("qjl_tree_attention", "n_draft", n_draft, (B,), torch.int32)
-    _index_tensor("qjl_tree_attention", "tree_mask", tree_mask, (B, N), torch.int64)
-    _device_tensors("qjl_tree_attention", Q, O, seqlens, n_draft, tree_mask, workspace, cache.tiles, draft.tiles)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = load_library().qjl_tree_attention(ctx, ctypes.byref(cache.struct()), ctypes.byref(draft.struct()), _ptr(Q),
-                                           *Q.stride()[:3], _dtype_code(Q), N, Hq, T, _ptr(seqlens), _ptr(n_draft),
-                                           _ptr(tree_mask), sm_scale, _ptr(O), _ptr(workspace), ws_bytes,
-                                           _stream(stream))
-    _check("qjl_tree_attention", st)
+    lens = _index_ptr(fn, "seqlens", seqlens, (B,), torch.int32)
+    drafts = _index_ptr(fn, "n_draft", n_draft, (B,), torch.int32)
+    mask = _index_ptr(fn, "tree_mask", tree_mask, (B, N), torch.int64)
+    cur = _current(fn, stream, Q, O, seqlens, n_draft, tree_mask, workspace, cache.tiles, draft.tiles)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    st = load_library().qjl_tree_attention(ctx, cache.struct(), draft.struct(), Q.data_ptr(), q[0], q[1], q[2],
+                                           _dtype_code(Q), N, Hq, T, lens, drafts, mask, sm_scale, O.data_ptr(), ws,
+                                           ws_bytes, cur)
+    if st:
+        _check(fn, st)
     return O
 
 
@@ -571,14 +589,15 @@ def qjl_cache_commit(ctx, cache: QJLCache, draft: QJLCache, path, n_accepted, se
     the others int32 [B]. seqlens_out (not seqlens itself) receives the new lengths."""
     import torch
 
-    _index_tensor("qjl_cache_commit", "path", path, (cache.B, path.shape[-1]), torch.int32)
+    fn = "qjl_cache_commit"
+    A, rows = path.shape[-1], (cache.B,)
+    ptrs = [_index_ptr(fn, "path", path, (cache.B, A), torch.int32)]
     for name, t in (("n_accepted", n_accepted), ("seqlens", seqlens), ("seqlens_out", seqlens_out)):
-        _index_tensor("qjl_cache_commit", name, t, (cache.B,), torch.int32)
-    _device_tensors("qjl_cache_commit", path, n_accepted, seqlens, seqlens_out, cache.tiles, draft.tiles)
-    st = load_library().qjl_cache_commit(ctx, ctypes.byref(cache.struct()), ctypes.byref(draft.struct()),
-                                         path.shape[1], _ptr(path), _ptr(n_accepted), _ptr(seqlens),
-                                         _ptr(seqlens_out), _stream(stream))
-    _check("qjl_cache_commit", st)
+        ptrs.append(_index_ptr(fn, name, t, rows, torch.int32))
+    cur = _current(fn, stream, path, n_accepted, seqlens, seqlens_out, cache.tiles, draft.tiles)
+    st = load_library().qjl_cache_commit(ctx, cache.struct(), draft.struct(), A, *ptrs, cur)
+    if st:
+        _check(fn, st)
     return seqlens_out
 
 
