@@ -6,12 +6,13 @@
 // int32 position, where an fp32 product would be off by whole radians near a
 // million; sin and cos are then taken in fp32 of the reduced turn.
 //
-// Bound: HBM, every element is read and written once. A thread owns two
-// 16-byte chunks of a head row that hold whole planes (chunks u and u +
-// rot/(2 e) in the half layout, u and u + d/(2 e) in the interleaved one, e
-// elements per chunk), computes their sines once and walks over heads, so the
-// fp64 work is paid once per token and not per head, and eight (bf16) lanes
-// cover 128 consecutive bytes with every load and store.
+// Bound: HBM, every element is read and written once. A block takes TT tokens
+// and all their heads: its threads compute the tokens' sines once into shared
+// memory (the fp64 work is paid per token, not per head), then a thread keeps
+// those of its two 16-byte chunks of a head row, which hold whole planes (chunks
+// u and u + rot/(2 e) in the half layout, u and u + d/(2 e) in the interleaved
+// one, e elements per chunk), and walks over the heads; eight (bf16) lanes cover
+// 128 consecutive bytes with every load and store.
 #include "qjl_internal.cuh"
 
 namespace qjl {
@@ -55,19 +56,29 @@ struct Chunk<float> {
   }
 };
 
-// Thread layout: consecutive threads take the pairs of one token's row, then
-// tokens; blockIdx.y takes a range of the call's heads.
-template <typename T, int LAYOUT>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p, int per) {
-  constexpr int E = Chunk<T>::n;            // elements of a chunk
+template <typename T, int LAYOUT, int TT>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int E = Chunk<T>::n;              // elements of a chunk
   constexpr int kPairs = kHeadDim / (2 * E);  // chunk pairs of a row
-  const int64_t gid = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x;
-  const int u = static_cast<int>(gid % kPairs);
-  const int64_t bt = gid / kPairs;
-  if (bt >= static_cast<int64_t>(p.B) * p.T) return;
-  const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt % p.T);
-  const int rot = p.table.rot_dim;
-  const int pos = p.positions ? p.positions[bt] : (p.t_start ? p.t_start[b] : 0) + t;
+  __shared__ float2 turn[TT][kHeadDim / 2];   // (cos, sin) of plane i of token k, the amplitude in both
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.T, tok0 = static_cast<int64_t>(blockIdx.x) * TT;
+  const int rot = p.table.rot_dim, half = rot / 2;
+  for (int e = threadIdx.x; e < TT * half; e += kRopeThreads) {
+    const int k = e / half, i = e - k * half;
+    const int64_t bt = tok0 + k;
+    if (bt >= tokens) break;
+    const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * p.T);
+    const int pos = p.positions ? p.positions[bt] : (p.t_start ? p.t_start[b] : 0) + t;
+    const double x = static_cast<double>(pos) * p.table.turns[i];
+    float sn, cs;
+    sincospif(static_cast<float>(2.0 * (x - rint(x))), &sn, &cs);  // half turns in [-1, 1]
+    turn[k][i] = make_float2(cs * p.table.amplitude, sn * (p.inverse ? -p.table.amplitude : p.table.amplitude));
+  }
+  __syncthreads();
+  const int u = threadIdx.x % kPairs, k = threadIdx.x / kPairs % TT;
+  const int64_t bt = tok0 + k;
+  if (bt >= tokens) return;
+  const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * p.T);
   // the thread's two chunks, and the first plane of each
   int c0, c1, plane0, plane1;
   if (LAYOUT == QJL_ROPE_HALF) {
@@ -85,23 +96,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   // half: cs/sn[k] of plane0 + k; interleaved: [0, E/2) of plane0 + k, [E/2, E) of plane1 + k
   float cs[E], sn[E];
 #pragma unroll
-  for (int k = 0; k < E; ++k) {
-    const int i = LAYOUT == QJL_ROPE_HALF ? plane0 + k : k < E / 2 ? plane0 + k : plane1 + k - E / 2;
-    const bool turn = LAYOUT == QJL_ROPE_HALF || k < E / 2 ? plane0 >= 0 : plane1 >= 0;
-    cs[k] = 1.0f;
-    sn[k] = 0.0f;
-    if (turn) {
-      const double x = static_cast<double>(pos) * p.table.turns[i];
-      const float r = static_cast<float>(2.0 * (x - rint(x)));  // half turns in [-1, 1]
-      sincospif(r, &sn[k], &cs[k]);
-      cs[k] *= p.table.amplitude;
-      sn[k] *= p.inverse ? -p.table.amplitude : p.table.amplitude;
-    }
+  for (int i = 0; i < E; ++i) {
+    const int pl = LAYOUT == QJL_ROPE_HALF || i < E / 2 ? plane0 : plane1;
+    const float2 v = pl >= 0 ? turn[k][pl + (LAYOUT == QJL_ROPE_HALF || i < E / 2 ? i : i - E / 2)] : make_float2(1.0f, 0.0f);
+    cs[i] = v.x;
+    sn[i] = v.y;
   }
   const int H = p.heads[0].H + (p.n_heads > 1 ? p.heads[1].H : 0);
-  const int h0 = blockIdx.y * per, h1 = min(H, h0 + per);
+  constexpr int kStep = kRopeThreads / (kPairs * TT);  // heads that the block takes at once
 #pragma unroll 4
-  for (int hh = h0; hh < h1; ++hh) {
+  for (int hh = threadIdx.x / (kPairs * TT); hh < H; hh += kStep) {
     const bool second = hh >= p.heads[0].H;
     const qjl_rope_heads& w = second ? p.heads[1] : p.heads[0];
     const int h = second ? hh - p.heads[0].H : hh;
@@ -138,31 +142,28 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
 }
 
-template <typename T>
-cudaError_t launch(const RopeParams& p, dim3 grid, int per, cudaStream_t s) {
+template <typename T, int TT>
+cudaError_t launch(const RopeParams& p, cudaStream_t s) {
+  const int64_t blocks = (static_cast<int64_t>(p.B) * p.T + TT - 1) / TT;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned n = static_cast<unsigned>(blocks);
   if (p.table.layout == QJL_ROPE_HALF)
-    rope_kernel<T, QJL_ROPE_HALF><<<grid, kRopeThreads, 0, s>>>(p, per);
+    rope_kernel<T, QJL_ROPE_HALF, TT><<<n, kRopeThreads, 0, s>>>(p);
   else
-    rope_kernel<T, QJL_ROPE_INTERLEAVED><<<grid, kRopeThreads, 0, s>>>(p, per);
+    rope_kernel<T, QJL_ROPE_INTERLEAVED, TT><<<n, kRopeThreads, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const RopeParams& p, cudaStream_t s) {
+  // four tokens a block fill it with whole planes of work; few tokens take a block each, for the SMs' sake
+  return static_cast<int64_t>(p.B) * p.T >= 4 * 148 ? launch<T, 4>(p, s) : launch<T, 1>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeParams& p, qjl_dtype dt, cudaStream_t s) {
-  const int H = p.heads[0].H + (p.n_heads > 1 ? p.heads[1].H : 0);
-  const int pairs = kHeadDim / (2 * (dt == QJL_BF16 ? 8 : 4));
-  const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
-  const int64_t blocks = (tokens * pairs + kRopeThreads - 1) / kRopeThreads;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  // heads per thread: as many as still leave two thousand threads per SM
-  constexpr int64_t kThreadsWanted = 148 * 2048;
-  const int64_t most = tokens * pairs * H / kThreadsWanted;
-  int per = static_cast<int>(most < 1 ? 1 : most < H ? most : H);
-  const int groups = (H + per - 1) / per;
-  per = (H + groups - 1) / groups;
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((H + per - 1) / per));
-  return dt == QJL_BF16 ? launch<__nv_bfloat16>(p, grid, per, s) : launch<float>(p, grid, per, s);
+  return dt == QJL_BF16 ? launch_t<__nv_bfloat16>(p, s) : launch_t<float>(p, s);
 }
 
 }  // namespace qjl
