@@ -390,8 +390,8 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, int* col, Op
   return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-// NBW: 16-row groups of a weight warp.
-template <int NBW>
+// NBW: 16-row groups of a weight warp; BITS: of a value code.
+template <int NBW, int BITS>
 __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid_constant__ TreeTcParams p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -480,23 +480,33 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
           fence_after();
           uint32_t dst = lane_addr + 32 * c.ck * ring;
           const int k1 = min(c.nk, k0 + c.ck);
-#pragma unroll 1
-          for (int kc = k0; kc < k1; ++kc, dst += 32) {
-            const int w0 = 2 * kc, w1 = w0 + 1;
-            uint32_t x0, x1;
-            if (even) {
-              const uint2 x = *reinterpret_cast<const uint2*>((w0 < wpt ? kb : ko) + w0);
-              x0 = x.x;
-              x1 = x.y;
-            } else {
-              x0 = w0 < wpt ? kb[w0] : ko[w0];
-              x1 = w1 < wpt ? kb[w1] : w1 < words ? ko[w1] : 0u;
-            }
+          if (even) {  // word pairs of one part
             uint32_t e[16];
-            expand_word(x0, w0 < wpt ? n_in : n_out, e);
-            st16(dst, e);
-            expand_word(x1, w1 < wpt ? n_in : n_out, e);
-            st16(dst + 16, e);
+            const int ki = min(k1, wpt >> 1);
+            int kc = k0;
+#pragma unroll 1
+            for (; kc < ki; ++kc, dst += 32) {
+              const uint2 x = reinterpret_cast<const uint2*>(kb)[kc];
+              expand_word(x.x, n_in, e);
+              st16(dst, e);
+              expand_word(x.y, n_in, e);
+              st16(dst + 16, e);
+            }
+#pragma unroll 1
+            for (; kc < k1; ++kc, dst += 32) {
+              const uint2 x = *reinterpret_cast<const uint2*>(ko + 2 * kc);
+              expand_word(x.x, n_out, e);
+              st16(dst, e);
+              expand_word(x.y, n_out, e);
+              st16(dst + 16, e);
+            }
+          } else {
+#pragma unroll 1
+            for (int w = 2 * k0; w < 2 * k1; ++w, dst += 16) {
+              uint32_t e[16];
+              expand_word(w < wpt ? kb[w] : w < words ? ko[w] : 0u, w < wpt ? n_in : n_out, e);
+              st16(dst, e);
+            }
           }
           wait_st();
           fence_before();
@@ -521,6 +531,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     int st = 0, vb = 0, item = 0;
     uint32_t sph = 0, vph = 1;
     const __half2 sixteenth = __float2half2_rn(0.0625f);
+    const uint32_t key = (tt & 7) << 4;
     for (bool more = any; more && ok; more = w.next(p), ++item)
       for (int u = w.u0; u < w.u1 && ok; ++u) {
         ok = bar_wait(&raw_full[st], sph, limit, err) && bar_wait(&pv_empty[vb], vph, limit, err);
@@ -531,18 +542,21 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         const uint32_t* szp = reinterpret_cast<const uint32_t*>(tile + t.tl.vsz + 16 * j);
         unsigned char* row = smem + L.v + vb * kVBytes + tt * 128;
         uint32_t bits = 0u;
+        const bool special = draft || w.tokens(u) < kUnit;
 #pragma unroll 2
         for (int g = 0; g < 4; ++g) {
-          // a masked drafted value that is not finite must not meet a weight of
-          // zero in the product: it is left out here and added at the end
-          const uint32_t sz = szp[g];
-          const bool off = draft && ((sz & 0x7C00u) == 0x7C00u || (sz & 0x7C000000u) == 0x7C000000u);
-          if (off) bits |= 1u << g;
-          const uint32_t use = live && !off ? sz : 0u;
+          uint32_t use = szp[g];
+          if (special) {
+            // a masked drafted value that is not finite must not meet a weight of
+            // zero in the product: it is left out here and added at the end
+            const bool off = draft && ((use & 0x7C00u) == 0x7C00u || (use & 0x7C000000u) == 0x7C000000u);
+            if (off) bits |= 1u << g;
+            if (!live || off) use = 0u;
+          }
           const __half2 s2 = __hmul2(__half2half2(__ushort_as_half(static_cast<unsigned short>(use))), sixteenth);
           const __half2 z2 = __hmul2(__half2half2(__ushort_as_half(static_cast<unsigned short>(use >> 16))), sixteenth);
           uint32_t lo[4], hi[4];  // codes of dims (8c + k, 8c + k + 4), k = 0..3, of 8-dim chunk c: two fields 16 bits apart
-          if (t.tl.vbits == 4) {
+          if (BITS == 4) {
             const uint4 cw = *reinterpret_cast<const uint4*>(tile + t.tl.vcode + j * (kHeadDim / 2) + 16 * vcode_chunk(j, g));
             const uint32_t cc[4] = {cw.x, cw.y, cw.z, cw.w};
 #pragma unroll
@@ -573,8 +587,8 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
               const __half2 r = __hfma2(n, s2, z2);
               y[e] = *reinterpret_cast<const uint32_t*>(&r);
             }
-            const int ch = 4 * g + k;  // 8-dim chunk
-            *reinterpret_cast<uint4*>(row + (ch >> 3) * kPlane + (((ch ^ tt) & 7) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            // 8-dim chunk 4 g + k of the row
+            *reinterpret_cast<uint4*>(row + (g >> 1) * kPlane + (((4 * (g & 1) + k) << 4) ^ key)) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
         if (draft && tt < 64) bad[64 * (item % kBadRing) + tt] = live ? bits : 0u;
@@ -1021,8 +1035,10 @@ cudaError_t launch_tree_attention_tc(const TreeParams& t, cudaStream_t s) {
   p.grid = static_cast<int>(most < t.num_sms ? most : t.num_sms);
   // one block per SM: it takes all tensor-memory columns
   const size_t smem = p.c.smem < 116 * 1024 ? 116 * 1024 : static_cast<size_t>(p.c.smem);
-  void (*const kernels[])(TreeTcParams) = {tree_tc_kernel<1>, tree_tc_kernel<2>, tree_tc_kernel<3>, tree_tc_kernel<4>};
-  void (*const kernel)(TreeTcParams) = kernels[(p.c.rb / 16 + 1) / 2 - 1];
+  void (*const kernels[])(TreeTcParams) = {
+      tree_tc_kernel<1, 4>, tree_tc_kernel<2, 4>, tree_tc_kernel<3, 4>, tree_tc_kernel<4, 4>,
+      tree_tc_kernel<1, 2>, tree_tc_kernel<2, 2>, tree_tc_kernel<3, 2>, tree_tc_kernel<4, 2>};
+  void (*const kernel)(TreeTcParams) = kernels[(t.tl.vbits == 4 ? 0 : 4) + (p.c.rb / 16 + 1) / 2 - 1];
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   tree_prepare_kernel<<<dim3(static_cast<unsigned>(p.c.nrb * p.c.rb / 16), static_cast<unsigned>(t.B * t.Hkv)),
