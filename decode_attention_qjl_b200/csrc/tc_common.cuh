@@ -19,6 +19,17 @@ __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
 __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -30,21 +41,20 @@ __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool bar_wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit,
-                                           volatile int* err) {
+// Wait for the phase with the given parity; false after `limit` SM clock
+// cycles, or once another waiter of the block has given up (*err). The first
+// look does not block, and the clock is read before every blocking try, so that
+// the shortest limit fails every wait that is not over when it begins.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile int* err) {
+  if (bar_test(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (bar_try(bar, parity)) return true;
-    if (static_cast<unsigned long long>(clock64() - t0) > limit || (err && *err)) {
+    if (static_cast<unsigned long long>(clock64() - t0) >= limit || (err && *err)) {
       if (err) *err = 1;
       return false;
     }
+    if (bar_try(bar, parity)) return true;
   }
-}
-// Wait for the phase with the given parity; false after `limit` SM clock
-// cycles, or once another waiter of the block has given up (*err).
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile int* err) {
-  return bar_try(bar, parity) || bar_wait_slow(bar, parity, limit, err);
 }
 
 // Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).

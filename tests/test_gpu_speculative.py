@@ -377,6 +377,80 @@ def test_chain_of_drafts_equals_decode_steps():
         assert err <= B16, (i, err)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tree_many_sequences_of_every_length(dtype):
+    """More sequences than a warp has lanes, empty ones and ones without drafts among them, in every place."""
+    B, N = 75, 3
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.choice([0, 0, 1, 2, 63, 64, 65, 127, 128, 129, 200, 300], B)]
+    nds = [int(x) for x in rng.integers(0, N + 1, B)]
+    nds[0] = nds[-1] = 0
+    lens[5], nds[5] = 0, 0
+    case = Case(B, 1, 2, 300, N, dtype)
+    mask = random_tree(B, N, 6)
+    check_tree(case, case.tree(mask, lens, nds), mask, lens, nds)
+    out = case.tree(mask, lens, [0] * B)
+    assert int(out.count_nonzero()) == 0  # nobody drafts: all rows are zero
+
+
+def test_tree_lengths_are_clamped_and_masks_of_64_drafts():
+    case = Case(2, 1, 1, 150, 64)
+    chain = [[(1 << (i + 1)) - 1 for i in range(64)] for _ in range(2)]
+    want = case.tree(chain)
+    assert torch.equal(case.tree(None), want)                                    # the default mask is the chain
+    assert torch.equal(case.tree(chain, [10 ** 6, 150], [64, 99]), want)         # past T and N
+    low = case.tree(chain, [-3, 0], [64, 64])
+    check_tree(case, low, chain, [0, 0], rows=6)
+    last = [[1 << 63] * 64 for _ in range(2)]                                    # only the last draft
+    check_tree(case, case.tree(last), last, rows=6)
+    none = case.tree(chain, [150, 150], [-1, 64])
+    assert int(none[0].count_nonzero()) == 0 and torch.equal(none[1], want[1])
+
+
+@pytest.mark.parametrize("g,N", [(1, 48), (2, 40), (4, 20), (4, 28), (8, 15), (8, 33)])
+def test_tree_row_blocks(g, N):
+    """48 to 264 rows of a kv head: every size of a row block, and several of them."""
+    case = Case(1, 2, g, 700, N, m=128, m_out=64)
+    mask = random_tree(1, N, N)
+    check_tree(case, case.tree(mask), mask, rows=5)
+
+
+def test_tree_logits_that_grow_along_the_context():
+    """Keys whose norms grow with the position: every unit raises the maximum, and with it the references."""
+    case = Case(1, 1, 4, 1500, 8, n_outlier=0, m_out=0)
+    off, nb, sec = next((o, n, s) for nm, o, n, s in Q.tile_sections(256, 0) if nm == "knorm")
+    v = case.cache.tiles[..., off:off + sec].unflatten(-1, (64, nb))
+    grow = (0.05 * torch.arange(v.shape[2] * 64, device="cuda").float()).half().view(1, 1, -1, 64)
+    pair = torch.stack([grow, torch.zeros_like(grow)], -1)
+    v.copy_(pair.contiguous().view(torch.uint8).reshape(1, 1, -1, 64, 4))
+    mask = random_tree(1, 8, 5)
+    check_tree(case, case.tree(mask), mask)
+    case.Q.mul_(8)
+    check_tree(case, case.tree(mask), mask)
+
+
+def test_tree_and_read_wait_limits():
+    """Waits that run out end the call with NaN rows (no fault, no hang); the next call is whole again."""
+    case = Case(2, 4, 4, 6000, 16)
+    mask = random_tree(2, 16, 7)
+    ws = case.ctx.tree_workspace(2, 16, 16, 4)
+    want = case.tree(mask, ws=ws)
+    K = torch.zeros(2, 4, 6000, D, dtype=torch.bfloat16, device="cuda")
+    Q.qjl_cache_read(case.ctx.handle, case.cache, 6000, K)
+    good = K.clone()
+    try:
+        Q.qjl_set_wait_limit(case.ctx.handle, 1)
+        out = case.tree(mask, ws=ws)
+        Q.qjl_cache_read(case.ctx.handle, case.cache, 6000, K)
+        torch.cuda.synchronize()
+        assert torch.isnan(out).any() and torch.isnan(K).any()
+    finally:
+        Q.qjl_set_wait_limit(case.ctx.handle, 2_000_000_000)
+    assert torch.equal(case.tree(mask, ws=ws), want)
+    Q.qjl_cache_read(case.ctx.handle, case.cache, 6000, K)
+    assert torch.equal(K, good)
+
+
 # ------------------------------------------------------------------ read
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -435,6 +509,24 @@ def test_cache_read_one_output_only_and_scores():
     want = np.einsum("bhgd,bhtd->bhgt", C.to64(case.Q[:, 0]).reshape(1, 2, 2, D), C.to64(K)).reshape(1, 4, 150)
     floor = C.SCORE_FLOOR * np.sqrt((want ** 2).mean(-1, keepdims=True))
     assert np.all(np.abs(sc - want) <= C.SCORE_RTOL * np.maximum(np.abs(want), floor))
+
+
+def test_cache_read_ranges():
+    """Starts before, inside and far past the cache, more tokens than it holds, strides of a wider buffer."""
+    case = Case(4, 2, 1, 300, 1, cap=320)
+    lens = torch.tensor([300, 300, 300, 128], dtype=torch.int32, device="cuda")
+    start = torch.tensor([-200, 299, 2 ** 31 - 10, 127], dtype=torch.int32, device="cuda")
+    full = torch.zeros(4, 2, 320, D, device="cuda")
+    Q.qjl_cache_read(case.ctx.handle, case.cache, 320, full, seqlens=torch.full_like(lens, 300))
+    T = 777
+    wide = torch.full((4, 2, T, 2, D), 5.0, device="cuda")
+    Q.qjl_cache_read(case.ctx.handle, case.cache, T, K_out=wide[:, :, :, 1], t_start=start, seqlens=lens)
+    want = torch.full_like(wide, 5.0)
+    want[0, :, 200:500, 1] = full[0, :, :300]
+    want[1, :, 0:1, 1] = full[1, :, 299:300]
+    want[3, :, 0:1, 1] = full[3, :, 127:128]
+    assert torch.equal(wide, want)
+    Q.qjl_cache_read(case.ctx.handle, case.cache, 0, K_out=wide[:, :, :0, 1])  # nothing
 
 
 # ------------------------------------------------------------------ commit
