@@ -445,17 +445,17 @@ RowStage<T, SEG> out{stage + 32 * SEG * (warp - 8), 0u, nullptr, p.v_st};
             if (!ok) break;
             fence_after();
           }
-          mma_ts_mn_32(tmem + (w < wpt ? 128 * buf : kReadColOut), ad, bd, id, w != 0 && w != wpt);
+          mma_ts_mn_32_warp(tmem + (w < wpt ? 128 * buf : kReadColOut), ad, bd, id, w != 0 && w != wpt);
         }
         if (!ok) break;
-        commit(&a_empty[ring]);
+        commit_warp(&a_empty[ring]);
         ring ^= 1;
         aph ^= ring == 0 ? 1u : 0u;
       }
-      if (ok) commit(&d_full[buf]);
+      if (ok) commit_warp(&d_full[buf]);
       ++units;
     }
-    commit(drain);  // every product ends before the block gives its memory back
+    commit_warp(drain);  // every product ends before the block gives its memory back
     bar_wait(drain, 0, limit > 2000000000ull ? limit : 2000000000ull, nullptr);
   }
   __syncwarp();

@@ -69,17 +69,24 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// tcgen05.commit and tcgen05.mma are called by a whole converged warp, whose
-// elected thread issues them: with the operands the same in every lane the
-// compiler keeps them in uniform registers, and an mma costs 19 cycles to issue
-// (128 x 64 x 16: 33, the tensor rate) where `if (lane == 0)` around it costs 48,
-// and 160 when other warps compete for the issue slots.
-__device__ __forceinline__ void commit(uint64_t* bar) {
+// One thread of a converged warp. commit and the products below are called by
+// that thread alone (the _warp forms by the warp), under `if (elect_one())` around the whole role: the
+// compiler then knows that one thread is active and moves operands straight to
+// uniform registers. An mma costs 16 cycles to issue this way (128 x 64 x 16: 32,
+// the tensor rate), 19 to 22 with an elect.sync per mma in a whole warp, and 48
+// under `if (lane == 0)`, or 160 when other warps compete for the issue slots.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
       "{\n\t.reg .pred e;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -127,36 +134,34 @@ __host__ __device__ constexpr uint32_t idesc_f16(int n, bool bf16, int a_mn, int
 }
 // Products of 64 (FULL) or 32 consecutive K values: A from tensor memory (8
 // columns per 16), B K-major in shared memory (32 bytes per 16). One asm block,
-// so that the thread is elected once and the steps are additions between
-// uniform registers.
+// so that the steps are additions between uniform registers.
 template <bool FULL>
 __device__ __forceinline__ void mma_ts_64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   if (FULL)
     asm volatile(
-        "{\n\t.reg .pred p, e, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
         "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
         "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
         "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p, e, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
         "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
         "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, 2;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
         : "memory");
 }
 // Products of 32 K values: A from tensor memory, B MN-major in shared memory.
-__device__ __forceinline__ void mma_ts_mn_32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+// Called by a whole converged warp; as is commit_warp.
+__device__ __forceinline__ void mma_ts_mn_32_warp(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n\t.reg .pred p, e, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
@@ -167,16 +172,22 @@ __device__ __forceinline__ void mma_ts_mn_32(uint32_t d, uint32_t a, uint64_t b,
       "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
+__device__ __forceinline__ void commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
 // Two products of 16 K values each with both operands MN-major in shared
 // memory (2048 bytes, 128 descriptor units, per 16).
 __device__ __forceinline__ void mma_ss_mn2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a1, b1;\n\t"
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 a1, b1;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "add.u64 a1, %1, 128;\n\tadd.u64 b1, %2, 128;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }

@@ -282,8 +282,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) tree_prepare_kernel(TreeTcPar
 
 // ---------------------------------------------------------------- main kernel
 
-// The items (sequence, kv head, row block) of a block's range of units, in order
-// (walked by whole warps).
+// The items (sequence, kv head, row block) of a block's range of units, in order.
 struct Walk {
   int b, hk, rbk;            // current item
   int len, nd, units, nblk;  // of sequence b
@@ -314,6 +313,8 @@ struct Walk {
     units = seq_units(p.t, b);
     nblk = (nd * p.t.G + p.c.rb - 1) / p.c.rb;
   }
+  // WARP: called by a whole warp, which makes the bounds uniform values
+  template <bool WARP>
   __device__ bool next(const TreeTcParams& p) {
     left -= u1 - u0;
     if (left <= 0) return false;
@@ -327,7 +328,8 @@ struct Walk {
       }
     }
     u0 = 0;
-    u1 = __shfl_sync(0xffffffffu, static_cast<int>(min(static_cast<long long>(units), left)), 0);
+    u1 = static_cast<int>(min(static_cast<long long>(units), left));
+    if (WARP) u1 = __shfl_sync(0xffffffffu, u1, 0);
     return true;
   }
   __device__ bool draft(int u) const { return u == units - 1; }
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     bool ok = true;
     int st = 0, ring = 0;
     uint32_t sph = 0, rph = 1;  // phases: stage full, chunk empty (the first pass finds every chunk empty)
-    for (bool more = any; more && ok; more = w.next(p))
+    for (bool more = any; more && ok; more = w.next<true>(p))
       for (int u = w.u0; u < w.u1 && ok; ++u) {
         ok = bar_wait(&raw_full[st], sph, limit, err);
         ok = __all_sync(0xffffffffu, ok);
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     uint32_t sph = 0, vph = 1;
     const __half2 sixteenth = __float2half2_rn(0.0625f);
     const uint32_t key = (tt & 7) << 4;
-    for (bool more = any; more && ok; more = w.next(p), ++item)
+    for (bool more = any; more && ok; more = w.next<true>(p), ++item)
       for (int u = w.u0; u < w.u1 && ok; ++u) {
         ok = bar_wait(&raw_full[st], sph, limit, err) && bar_wait(&pv_empty[vb], vph, limit, err);
         ok = __all_sync(0xffffffffu, ok);
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     int n = 0;            // units so far
     uint32_t oph = 0;
     int it = 0;
-    for (bool more = any; more; more = w.next(p), ++it) {
+    for (bool more = any; more; more = w.next<true>(p), ++it) {
       const int64_t item = w.bh(p) * c.nrb + w.rbk;
       uint64_t lsum[NBW][8];  // sums of this token's weights, pairs of rows
 #pragma unroll
@@ -851,8 +853,8 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == kMmaWarp) {
-      // ========================================================== products (the whole warp, converged)
+    if (warp == kMmaWarp && elect_one()) {
+      // ========================================================== products
       bool ok = true;
       int n = 0, ring = 0, item = 0;
       uint32_t aph = 0;
@@ -863,7 +865,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       const uint32_t sq_bytes = static_cast<uint32_t>(c.nk) * c.rb * 128;
       bool sq_out = false;  // a copy of the projected queries is in flight
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, err));
+        if (ok) ok = bar_wait(bar, parity, limit, err);
       };
       auto values = [&](int q, bool first_u, bool last_u) {  // O += V^T P of unit q
         const int pb = c.np == 2 ? q & 1 : 0, vb = q & 1;
@@ -878,14 +880,11 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         commit(&pv_empty[vb]);
         if (last_u) commit(o_full);
       };
-      for (bool more = any; more && ok; more = w.next(p), ++item) {
+      for (bool more = any; more && ok; more = w.next<false>(p), ++item) {
         // the last item's score products are done: its logits were read (s_full was waited for by the weights, and
         // `values` of its last unit waited for those)
-        if (lane == 0) {
-          bar_expect(sq_full, sq_bytes);
-          bulk_load(sq_base, p.image + (w.bh(p) * c.nrb + w.rbk) * static_cast<int64_t>(sq_bytes), sq_bytes, sq_full);
-        }
-        __syncwarp();
+        bar_expect(sq_full, sq_bytes);
+        bulk_load(sq_base, p.image + (w.bh(p) * c.nrb + w.rbk) * static_cast<int64_t>(sq_bytes), sq_bytes, sq_full);
         sq_out = true;
         wait(sq_full, item & 1);
         if (!ok) break;
@@ -925,7 +924,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       bool ok = true;
       int st = 0, issued = 0;
       uint32_t eph = 1;
-      for (bool more = any; more && ok; more = w.next(p)) {
+      for (bool more = any; more && ok; more = w.next<true>(p)) {
         const int64_t bh = w.bh(p);
         for (int u = w.u0; u < w.u1; ++u) {
           ok = __all_sync(0xffffffffu, bar_wait(&raw_empty[st], eph, limit, err));
