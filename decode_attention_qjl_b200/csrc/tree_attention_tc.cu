@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         unsigned char* row = smem + L.v + vb * kVBytes + tt * 128;
         uint32_t bits = 0u;
         const bool special = draft || w.tokens(u) < kUnit;
-#pragma unroll 2
+#pragma unroll 4
         for (int g = 0; g < 4; ++g) {
           uint32_t use = szp[g];
           if (special) {
