@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kReadThreads, 1) cache_read_kernel(const __gri
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     // S, S_out -> the B operand: row 32 w + expand_pos(i) holds projection 32 w + i, two planes of 64 channels
+#pragma unroll 4
     for (int e = tid; e < rows * 16; e += kReadThreads) {
       const int i = e >> 4, ch = e & 15;
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(i < p.m ? p.S + i * kHeadDim : p.S_out + (i - p.m) * kHeadDim) + ch);

@@ -966,46 +966,70 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
 
 // One warp per output row: rows past the drafts are zero, rows of an item that
 // one block held whole are already written, the others are joined from the
-// parts of the blocks cta(u0) .. cta(u1 - 1) that share the item.
+// parts of the blocks that share the item, four parts in flight at a time. In
+// 32 bits: the units of any cache that a device holds fit 31.
 __global__ void __launch_bounds__(256) tree_join_kernel(TreeTcParams p) {
   griddep_wait();
   const TreeParams& t = p.t;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int row = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5);  // (at most 65535 * 8 * 64)
   const int lane = threadIdx.x & 31;
-  if (row >= static_cast<int64_t>(t.B) * t.N * t.Hq) return;
-  const int h = static_cast<int>(row % t.Hq), i = static_cast<int>(row / t.Hq % t.N);
-  const int b = static_cast<int>(row / t.Hq / t.N);
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(t.O) + row * kHeadDim + 4 * lane;
-  if (i >= seq_drafts(t, b)) {
+  if (row >= t.B * t.N * t.Hq) return;
+  const int bi = row / t.Hq, h = row - bi * t.Hq, b = bi / t.N, i = bi - b * t.N;
+  const int total = static_cast<int>(p.start[t.B]), nd = seq_drafts(t, b), units = seq_units(t, b);
+  int u0 = static_cast<int>(p.start[b]);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(t.O) + static_cast<int64_t>(row) * kHeadDim + 4 * lane;
+  if (i >= nd) {
     *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
     return;
   }
-  const int r = i * t.G + h % t.G, units = seq_units(t, b);
-  const int nblk = (seq_drafts(t, b) * t.G + p.c.rb - 1) / p.c.rb;
-  const long long u0 = p.start[b] + (static_cast<long long>(h / t.G) * nblk + r / p.c.rb) * units;
-  const long long total = p.start[t.B];
-  const long long c0 = ((u0 + 1) * p.grid - 1) / total, c1 = ((u0 + units) * p.grid - 1) / total;
+  const int hk = h / t.G, r = i * t.G + h - hk * t.G, rbk = r / p.c.rb, col = r - rbk * p.c.rb;
+  u0 += (hk * ((nd * t.G + p.c.rb - 1) / p.c.rb) + rbk) * units;
+  // the block of unit u: floor(((u + 1) grid - 1) / total); the quotient of these exact doubles is off by less than
+  // its distance to an integer, 1 / total
+  auto block_of = [&](int u) {
+    return static_cast<int>((static_cast<double>(u + 1) * p.grid - 1.0) / static_cast<double>(total));
+  };
+  const int c0 = block_of(u0), c1 = block_of(u0 + units - 1);
   if (c0 == c1) return;
-  const int col = r % p.c.rb;
-  auto slot = [&](long long c) { return 2 * c + (total * c / p.grid < u0 ? 1 : 0); };
-  // (with fewer units than blocks some of them have none)
-  auto idle = [&](long long c) { return total * (c + 1) / p.grid == total * c / p.grid; };
+  const int q = total / p.grid, rest = total - q * p.grid;
+  auto first = [&](int c) { return q * c + rest * c / p.grid; };  // first unit of block c
   float M = -kNothing, L = 0.0f;
-  for (long long c = c0; c <= c1; ++c)
-    if (!idle(c)) M = fmaxf(M, p.part_ml[slot(c) * p.c.rb + col].x);
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (long long c = c0; c <= c1; ++c) {
-    if (idle(c)) continue;
-    const int64_t s = slot(c) * p.c.rb + col;
-    const float2 ml = p.part_ml[s];
-    if (ml.y == 0.0f) continue;  // nothing seen (a NaN sum stays)
-    const float f = ml.x == M ? 1.0f : exp2f(ml.x - M);
-    const float4 o = reinterpret_cast<const float4*>(p.part_o)[s * (kHeadDim / 4) + lane];
-    L = fmaf(ml.y, f, L);
-    acc.x = fmaf(o.x, f, acc.x);
-    acc.y = fmaf(o.y, f, acc.y);
-    acc.z = fmaf(o.z, f, acc.z);
-    acc.w = fmaf(o.w, f, acc.w);
+  for (int c = c0; c <= c1; c += 4) {
+    float2 ml[4];
+    float4 o[4];
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      ml[k] = make_float2(-kNothing, 0.0f);
+      o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const int s0 = first(c + k);
+      // (with more blocks than units some of them have none)
+      if (c + k <= c1 && s0 != first(c + k + 1)) {
+        const int s = (2 * (c + k) + (s0 < u0 ? 1 : 0)) * p.c.rb + col;
+        ml[k] = p.part_ml[s];
+        o[k] = reinterpret_cast<const float4*>(p.part_o)[static_cast<int64_t>(s) * (kHeadDim / 4) + lane];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+    const float f = M == top ? 1.0f : exp2f(M - top);
+    M = top;
+    L *= f;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (ml[k].y == 0.0f) continue;  // nothing seen (a NaN sum stays)
+      const float g = ml[k].x == M ? 1.0f : exp2f(ml[k].x - M);
+      L = fmaf(ml[k].y, g, L);
+      acc.x = fmaf(o[k].x, g, acc.x);
+      acc.y = fmaf(o[k].y, g, acc.y);
+      acc.z = fmaf(o[k].z, g, acc.z);
+      acc.w = fmaf(o[k].w, g, acc.w);
+    }
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);

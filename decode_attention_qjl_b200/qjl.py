@@ -459,7 +459,7 @@ def _current(fn: str, stream, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"{fn}: tensor on {t.device}, the call runs on cuda:{cur}")
-    return torch.cuda.current_stream(cur).cuda_stream if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream
 
 
 def _index_ptr(fn: str, name: str, t, shape, dtype):
