@@ -140,7 +140,7 @@ __device__ __forceinline__ int seq_items(const TreeParams& t, const TreeTcCfg& c
 // row's largest entry lies in [2^14, 2^15), rounded to fp16 and written in the
 // order and swizzle of the score product's B operand. Block (0, 0) also writes
 // the first unit of every sequence.
-constexpr int kPrepWarps = 8;
+constexpr int kPrepWarps = 12;
 constexpr int kPrepWords = (kMaxM + kMaxMOut) / 32 / kPrepWarps;  // sign words of a warp
 
 __global__ void __launch_bounds__(32 * kPrepWarps) tree_prepare_kernel(TreeTcParams p) {
@@ -169,6 +169,11 @@ __global__ void __launch_bounds__(32 * kPrepWarps) tree_prepare_kernel(TreeTcPar
   const int row0 = blockIdx.x * 16;                    // rows of nrb * rb
   if ((row0 / p.c.rb) * p.c.rb >= live) return;        // a row block nobody computes
   __shared__ float top_s[kPrepWarps][16];
+  const int words_all = (t.m + t.m_out) / 32;
+  uint4 first_s[16];  // the warp's first word, fetched ahead of what its use depends on
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    first_s[k] = warp < words_all ? __ldg(t.S_frag + (16 * warp + k) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
   uint32_t om[4] = {0u, 0u, 0u, 0u};
   {
     const int c = lane < t.n_out ? min(max(t.idx[bh * t.n_out + lane], 0), kHeadDim - 1) : -1;
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) tree_prepare_kernel(TreeTcPar
       for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          const uint4 a = __ldg(t.S_frag + ((2 * w + hf) * 8 + ks) * 32 + lane);
+          const uint4 a = s == 0 ? first_s[8 * hf + ks] : __ldg(t.S_frag + ((2 * w + hf) * 8 + ks) * 32 + lane);
           const uint32_t k0 = second ? ~keep[ks][0] : keep[ks][0], k1 = second ? ~keep[ks][1] : keep[ks][1];
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
