@@ -57,7 +57,7 @@ struct Chunk<float> {
 };
 
 template <typename T, int LAYOUT, int TT>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int E = Chunk<T>::n;              // elements of a chunk
   constexpr int kPairs = kHeadDim / (2 * E);  // chunk pairs of a row
   __shared__ float2 turn[TT][kHeadDim / 2];   // (cos, sin) of plane i of token k, the amplitude in both
