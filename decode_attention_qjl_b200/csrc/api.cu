@@ -2,12 +2,13 @@
 // kernel launches. Every entry point is declared and documented in qjl.h.
 #include <cmath>
 #include <limits>
+#include <map>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <new>
 #include <string>
-#include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "qjl_internal.cuh"
@@ -116,11 +117,14 @@ void set_last_error(const std::string& msg) { g_last_error = msg; }
 
 cudaError_t ensure_smem_limit(const void* func, size_t bytes) {
   static std::mutex mu;
-  static std::unordered_map<const void*, size_t> configured;  // per kernel, per process (one device)
+  static std::map<std::pair<const void*, int>, size_t> configured;  // per kernel and device (the attribute is a device's)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
-  size_t& cur = configured[func];
+  size_t& cur = configured[{func, dev}];
   if (bytes <= cur) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   if (e == cudaSuccess) cur = bytes;
   return e;
 }

