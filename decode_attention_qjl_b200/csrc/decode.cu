@@ -1028,7 +1028,7 @@ __global__ void __launch_bounds__(Shape<G>::THREADS, 1) decode_kernel(DecodePara
           ++gs;
         }
       }
-      if (pend) await_prep();  // query blocks still to copy
+      await_prep();  // query blocks still to copy; and this grid never ends before the prep grid
       // Drain: every copy issued here lands before the CTA may exit (a query
       // block is copied only once the consumers released the block two
       // segments back, so only the last one per buffer can be in flight).
