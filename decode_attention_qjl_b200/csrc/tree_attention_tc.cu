@@ -148,16 +148,26 @@ __device__ __forceinline__ int seq_items(const TreeParams& t, const TreeTcCfg& c
 // decode's A-fragment order, products exact, fp32 sums), scaled so that the
 // row's largest entry lies in [2^14, 2^15), rounded to fp16 and written in the
 // order and swizzle of the score product's B operand. Block (0, 0) also writes
-// the first unit of every sequence.
+// the first unit of every sequence. Launched before what precedes it ends, it
+// waits for that before it touches anything but S: 1.4 us less at 130 tokens,
+// 2 us less at 1024 (19.2 -> 17.8, 36.2 -> 34.0).
 constexpr int kPrepWarps = 12;
 constexpr int kPrepWords = (kMaxM + kMaxMOut) / 32 / kPrepWarps;  // sign words of a warp
 
 __global__ void __launch_bounds__(32 * kPrepWarps) tree_prepare_kernel(TreeTcParams p) {
-  griddep_launch();
   const TreeParams& t = p.t;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t bh = blockIdx.y;
   const int b = static_cast<int>(bh / t.Hkv), hk = static_cast<int>(bh % t.Hkv);
+  uint4 first_s[16];  // the warp's first word of [S; S_out], which no kernel writes, ahead of the wait
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    first_s[k] = warp < (t.m + t.m_out) / 32 ? __ldg(t.S_frag + (16 * warp + k) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+  // whatever came before on the stream may write the inputs and read the
+  // workspace; the next kernel is let in after it too, so that one which holds
+  // all tensor memory never meets one still to allocate its own
+  griddep_wait();
+  griddep_launch();
   if (blockIdx.x == 0 && bh == 0 && warp == 0) {
     long long base = 0;
     for (int b0 = 0; b0 < t.B; b0 += 32) {
@@ -178,11 +188,6 @@ __global__ void __launch_bounds__(32 * kPrepWarps) tree_prepare_kernel(TreeTcPar
   const int row0 = blockIdx.x * 16;                    // rows of nrb * rb
   if ((row0 / p.c.rb) * p.c.rb >= live) return;        // a row block nobody computes
   __shared__ float top_s[kPrepWarps][16];
-  const int words_all = (t.m + t.m_out) / 32;
-  uint4 first_s[16];  // the warp's first word, fetched ahead of what its use depends on
-#pragma unroll
-  for (int k = 0; k < 16; ++k)
-    first_s[k] = warp < words_all ? __ldg(t.S_frag + (16 * warp + k) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
   uint32_t om[4] = {0u, 0u, 0u, 0u};
   {
     const int c = lane < t.n_out ? min(max(t.idx[bh * t.n_out + lane], 0), kHeadDim - 1) : -1;
@@ -1078,20 +1083,20 @@ cudaError_t launch_tree_attention_tc(const TreeParams& t, cudaStream_t s) {
   void (*const kernel)(TreeTcParams) = kernels[(t.tl.vbits == 4 ? 0 : 4) + (p.c.rb / 16 + 1) / 2 - 1];
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  tree_prepare_kernel<<<dim3(static_cast<unsigned>(p.c.nrb * p.c.rb / 16), static_cast<unsigned>(t.B * t.Hkv)),
-                        32 * kPrepWarps, 0, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
-  cfg.blockDim = dim3(kTreeTcThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.c.nrb * p.c.rb / 16), static_cast<unsigned>(t.B * t.Hkv));
+  cfg.blockDim = dim3(32 * kPrepWarps);
+  e = cudaLaunchKernelEx(&cfg, tree_prepare_kernel, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
+  cfg.blockDim = dim3(kTreeTcThreads);
+  cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(t.B) * t.N * t.Hq;

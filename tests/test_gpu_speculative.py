@@ -672,6 +672,66 @@ def test_captured_steps_and_streams(dtype):
     assert new.tolist() == [402, 124]
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("before", ["nothing", "copy", "memset", "kernel", "join", "decode", "tree"])
+def test_tree_waits_for_what_came_before(before, captured):
+    """The call's first kernel may start early: whatever precedes it on the stream is done before it reads or writes."""
+    case = Case(2, 2, 4, 300, 4, cap=320)
+    ws = case.ctx.tree_workspace(2, 4, 8, 2)
+    q, out, alt = torch.empty_like(case.Q), torch.empty_like(case.Q), case.Q.float().mul(0.5).to(torch.bfloat16)
+    lens, big = torch.empty(2, dtype=torch.int32, device="cuda"), torch.ones(1 << 26, device="cuda")
+    dec_ws, o = case.ctx.decode_workspace(2, 8, 2, 320), torch.empty(2, 8, D, device="cuda")
+    none = torch.zeros(2, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    h = case.ctx.handle
+    full = [300, 200]
+    want = {"memset": case.tree(None, [0, 0]), "nothing": case.tree(None, full)}
+
+    def call(src):
+        if before == "copy":
+            big.mul_(1.0)
+            q.copy_(src)
+        elif before == "memset":
+            big.mul_(1.0)
+            lens.zero_()
+        elif before == "kernel":
+            big.mul_(1.0)
+            torch.mul(src, 1.0, out=q)
+        elif before == "join":  # the last writer is on another stream
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                big.mul_(1.0)
+                torch.mul(src, 1.0, out=q)
+            torch.mul(alt, 1.0, out=out)
+            torch.cuda.current_stream().wait_stream(side)
+        elif before == "decode":  # of empty sequences: no block of it has work
+            Q.qjl_decode_attention(h, case.cache, case.Q[:, 0].contiguous(), 300, o, seqlens=none, workspace=dec_ws)
+        elif before == "tree":  # the same workspace and output, other queries
+            Q.qjl_tree_attention(h, case.cache, case.draft, alt, 300, out, seqlens=lens, workspace=ws)
+        Q.qjl_tree_attention(h, case.cache, case.draft, q, 300, out, seqlens=lens, workspace=ws)
+
+    def reset():
+        late = before in ("copy", "kernel", "join")
+        q.zero_() if late else q.copy_(case.Q)
+        lens.copy_(torch.tensor(full, dtype=torch.int32))
+        out.fill_(float("nan"))
+
+    reset()
+    call(case.Q)
+    torch.cuda.synchronize()
+    graph = None
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(case.Q)
+    for _ in range(4):
+        reset()
+        torch.cuda.synchronize()
+        graph.replay() if captured else call(case.Q)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want.get(before, want["nothing"]))
+
+
 def test_refusals_on_the_gpu():
     case = Case(2, 2, 4, 100, 4)
     h, c, d, q = case.ctx.handle, case.cache, case.draft, case.Q
