@@ -180,15 +180,17 @@ __device__ __forceinline__ void commit_warp(uint64_t* bar) {
       : "memory");
 }
 // Two products of 16 K values each with both operands MN-major in shared
-// memory (2048 bytes, 128 descriptor units, per 16).
+// memory (2048 bytes, 128 descriptor units, per 16), added to the accumulator
+// times 2^-DOWN.
+template <int DOWN>
 __device__ __forceinline__ void mma_ss_mn2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n\t.reg .pred p, t;\n\t.reg .b64 a1, b1;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "add.u64 a1, %1, 128;\n\tadd.u64 b1, %2, 128;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p, %5;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "n"(DOWN)
       : "memory");
 }
 

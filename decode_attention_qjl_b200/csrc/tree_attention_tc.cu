@@ -26,8 +26,15 @@
 //
 // Softmax: p = 2^(x - ref) with ref = (maximum seen) - 4, moved only when a
 // logit passes ref + 15: weights stay below 2^15 in fp16, and those down to
-// 2^-18 of the largest keep all their bits. Values are kept as V_hat / 16,
-// which no fp16 scale and zero can push past the fp16 range. All sums are fp32.
+// 2^-18 of the largest keep all their bits; smaller ones are rounded to
+// multiples of 2^-28 of it at worst, so that n of them move an output by
+// n 2^-29 max |V_hat| at most. V_hat is a multiple of 2^-24, as its scale and
+// zero are: fp16 holds a value below 65504 to 2^-11 of itself, and exactly below
+// 2^-13. From the first unit with a token that may pass 65504 on (wide_token),
+// the values of an item are kept as V_hat / 16, which no fp16 scale and zero push
+// past the range, to 2^-11 or 2^-20 absolute; that unit's product divides the
+// outputs so far by 16. (Dividing from the start lost the bits of small values;
+// looking for wide tokens costs 1 to 2 % of the long cases.) All sums are fp32.
 //
 // Bound: HBM below about 35 rows of a kv head (124 bytes against 896 flops per
 // row and token), the tensor rate above. Measured, 4 x 131072 tokens, 8 kv heads,
@@ -67,7 +74,7 @@ struct TreeTcCfg {
   int smem;
 };
 constexpr int kBadRing = 4;  // items whose drafted values may be in flight at once (three)
-constexpr int kMiscBytes = 3 * 128 * 4 + 4 * 128 * 4 + 2 * 128 * 8 + kBadRing * 64 * 4 + 40 * 8 + 64;
+constexpr int kMiscBytes = 3 * 128 * 4 + 4 * 128 * 4 + 2 * 128 * 8 + kBadRing * 64 * 4 + (kBadRing + 2) * 4 + 32 * 8 + 64;
 
 // Row block, buffers and stages: the largest row block (fewest passes over the
 // cache) that leaves two stages, then a second weight buffer, then stages.
@@ -357,7 +364,7 @@ struct Walk {
 };
 
 struct TreeTcSmem {
-  int sq, v, pw, raw, rowc, lsum, cmax, mask, bad, bars, misc;
+  int sq, v, pw, raw, rowc, cmax, mask, bad, wide, bars, misc;
   __device__ explicit TreeTcSmem(const TreeTcCfg& c) {
     sq = 0;
     v = c.nk * c.rb * 128;
@@ -367,8 +374,9 @@ struct TreeTcSmem {
     cmax = rowc + 3 * 128 * 4;    // float [4][128]: column maxima, then sums, of the lane quarters
     mask = cmax + 4 * 128 * 4 + 128 * 8;  // (after int64 [128]: where a row's outputs go) uint64 [128]
     bad = mask + 128 * 8;         // uint32 [kBadRing][64]: value groups of a drafted token that are not finite
-    bars = bad + kBadRing * 64 * 4;
-    misc = bars + 40 * 8;
+    wide = bad + kBadRing * 64 * 4;      // int [kBadRing]: the item's values are divided by 16; int [2]: since this unit
+    bars = wide + (kBadRing + 2) * 4;
+    misc = bars + 32 * 8;
   }
 };
 
@@ -393,6 +401,19 @@ __device__ __forceinline__ bool s_any(int half, bool x) {
 }
 __device__ __forceinline__ void s_sync(int half) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 
+__device__ __forceinline__ bool v_any(bool x) {  // the value warps
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred p, 3, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 // Reduces 16 values per lane over the 32 lanes, value k ending in lanes
 // 2 rev(k), 2 rev(k) + 1; returns the column of this lane.
 template <typename Op>
@@ -409,6 +430,16 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, int* col, Op
   }
   *col = (lane & 16 ? 8 : 0) + (lane & 8 ? 4 : 0) + (lane & 4 ? 2 : 0) + (lane & 2 ? 1 : 0);
   return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+
+// zero + code * scale of one of a token's groups may pass 65504: a finite scale
+// of 2^11 or a finite zero of 2^15 and more (below, 15 * 2^11 + 2^15 < 65504).
+// Adding 2^10 to the bit patterns lets those that are not finite wrap to small ones.
+__device__ __forceinline__ bool wide_token(const uint4& sz) {
+  const uint32_t abs2 = 0x7FFF7FFFu, one = 0x04000400u;
+  const uint32_t top = __vmaxu2(__vmaxu2((sz.x + one) & abs2, (sz.y + one) & abs2),
+                                __vmaxu2((sz.z + one) & abs2, (sz.w + one) & abs2));
+  return (top & 0xFFFFu) >= 0x6C00u || top >= 0x7C000000u;
 }
 
 // NBW: 16-row groups of a weight warp; BITS: of a value code.
@@ -452,6 +483,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     bar_init(o_empty, kSWarps);
     bar_init(drain, 1);
     *err = 0;
+    for (int k = 0; k < 2; ++k) reinterpret_cast<int*>(smem + L.wide)[kBadRing + k] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -549,24 +581,39 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     const int tt = 32 * (warp - kKWarps) + lane, j = tt & 63;
     uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L.bad);
     bool ok = true;
-    int st = 0, vb = 0, item = 0;
+    int st = 0, vb = 0, item = 0, n = 0;
     uint32_t sph = 0, vph = 1;
-    const __half2 sixteenth = __float2half2_rn(0.0625f);
+    int* wides = reinterpret_cast<int*>(smem + L.wide);
     const uint32_t key = (tt & 7) << 4;
-    for (bool more = any; more && ok; more = w.next<true>(p), ++item)
+    for (bool more = any; more && ok; more = w.next<true>(p), ++item) {  // (ok ends for all four warps at once)
+      bool wide = false;  // the item's values are divided by 16 from here on
+      if (tt == 0) wides[item % kBadRing] = 0;
       for (int u = w.u0; u < w.u1 && ok; ++u) {
         ok = bar_wait(&raw_full[st], sph, limit, err) && bar_wait(&pv_empty[vb], vph, limit, err);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
         const unsigned char* tile = smem + L.raw + st * c.stage + (tt >> 6) * t.tl.bytes;
         const bool live = tt < w.tokens(u), draft = w.draft(u);
-        const uint32_t* szp = reinterpret_cast<const uint32_t*>(tile + t.tl.vsz + 16 * j);
+        const uint4 sz = *reinterpret_cast<const uint4*>(tile + t.tl.vsz + 16 * j);
+        const uint32_t* szg = reinterpret_cast<const uint32_t*>(tile + t.tl.vsz + 16 * j);
+        if (v_any(!ok | (live & wide_token(sz)))) {  // seldom: a wide token, or a wait that ran out
+          ok = !v_any(!ok);
+          if (!ok) break;
+          if (!wide && tt == 0) {
+            wides[item % kBadRing] = 1;
+            if (u > w.u0) wides[kBadRing + vb] = n;
+          }
+          wide = true;
+        }
+        // from a code's bits to the code, or to the code / 16 (exact, as is its product with the scale inside the fma;
+        // a zero / 16 below 2^-14 rounds by 2^-25 at most)
+        const __half2 odd_mul = __float2half2_rn(wide ? 0.00390625f : 0.0625f), odd_add = __float2half2_rn(wide ? -4.0f : -64.0f);
+        const __half2 even_mul = __float2half2_rn(wide ? 0.0625f : 1.0f), even_add = __float2half2_rn(wide ? -64.0f : -1024.0f);
         unsigned char* row = smem + L.v + vb * kVBytes + tt * 128;
         uint32_t bits = 0u;
         const bool special = draft || w.tokens(u) < kUnit;
-#pragma unroll 4
+#pragma unroll 2
         for (int g = 0; g < 4; ++g) {
-          uint32_t use = szp[g];
+          uint32_t use = szg[g];
           if (special) {
             // a masked drafted value that is not finite must not meet a weight of
             // zero in the product: it is left out here and added at the end
@@ -574,8 +621,8 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
             if (off) bits |= 1u << g;
             if (!live || off) use = 0u;
           }
-          const __half2 s2 = __hmul2(__half2half2(__ushort_as_half(static_cast<unsigned short>(use))), sixteenth);
-          const __half2 z2 = __hmul2(__half2half2(__ushort_as_half(static_cast<unsigned short>(use >> 16))), sixteenth);
+          const __half2 s2 = __half2half2(__ushort_as_half(static_cast<unsigned short>(use)));
+          const __half2 z2 = __hmul2(__half2half2(__ushort_as_half(static_cast<unsigned short>(use >> 16))), even_mul);
           uint32_t lo[4], hi[4];  // codes of dims (8c + k, 8c + k + 4), k = 0..3, of 8-dim chunk c: two fields 16 bits apart
           if (BITS == 4) {
             const uint4 cw = *reinterpret_cast<const uint4*>(tile + t.tl.vcode + j * (kHeadDim / 2) + 16 * vcode_chunk(j, g));
@@ -604,7 +651,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const __half2 h = *reinterpret_cast<const __half2*>(&f[e]);
-              const __half2 n = e & 1 ? __hfma2(h, sixteenth, __float2half2_rn(-64.0f)) : __hsub2(h, __float2half2_rn(1024.0f));
+              const __half2 n = e & 1 ? __hfma2(h, odd_mul, odd_add) : __hfma2(h, even_mul, even_add);
               const __half2 r = __hfma2(n, s2, z2);
               y[e] = *reinterpret_cast<const uint32_t*>(&r);
             }
@@ -620,12 +667,14 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
           bar_arrive(&raw_empty[st]);
         }
         vb ^= 1;
+        ++n;
         if (vb == 0) vph ^= 1u;
         if (++st == c.ns) {
           st = 0;
           sph ^= 1u;
         }
       }
+    }
   } else if (warp < kMmaWarp) {
     // ============================================================ weights
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWeights));
@@ -821,6 +870,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
       const long long item_start = first + ((end - first) - w.left) - w.u0;  // first unit of the item
       const int slot = 2 * blockIdx.x + (first < item_start ? 1 : 0);
       const float nan = __int_as_float(0x7fc00000);
+      const float unit = reinterpret_cast<const int*>(smem + L.wide)[it % kBadRing] ? 16.0f : 1.0f;  // of the outputs
       // per row: where its dims go (-1: a row past the drafts) and the factor of its outputs
       long long* dest = reinterpret_cast<long long*>(cmax + 512 - col0) + col0;
       if (stid < 16 * nbw) {
@@ -828,10 +878,10 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         const float sum = (cmax[stid] + cmax[128 + stid]) + (cmax[256 + stid] + cmax[384 + stid]);
         if (whole) {
           dest[stid] = ((static_cast<long long>(w.b) * t.N + i) * t.Hq + w.hk * t.G + g) * kHeadDim;
-          fac[stid] = !fine ? nan : sum == 0.0f ? 0.0f : 16.0f / sum;
+          fac[stid] = !fine ? nan : sum == 0.0f ? 0.0f : unit / sum;
         } else {
           dest[stid] = (static_cast<long long>(slot) * c.rb + col) * kHeadDim;
-          fac[stid] = fine ? 16.0f : nan;
+          fac[stid] = fine ? unit : nan;
           p.part_ml[slot * c.rb + col] =
               make_float2(-reinterpret_cast<const float*>(rowc)[4 * (stid >> 1) + 2 + (stid & 1)], fine ? sum : nan);
         }
@@ -893,9 +943,12 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         if (!ok) return;
         fence_after();
         const uint64_t vd = desc_mn(v_base + vb * kVBytes, kPlane), pd = desc_mn(p_base + pb * p_bytes, kPlane);
+        const volatile int* turns = reinterpret_cast<const int*>(smem + L.wide) + kBadRing;
+        if (turns[vb] == q) mma_ss_mn2<4>(tmem + col_o, vd, pd, id_o, true);  // the outputs so far divided by 16
+        else mma_ss_mn2<0>(tmem + col_o, vd, pd, id_o, !first_u);
 #pragma unroll
-        for (int ks = 0; ks < kUnit / 16; ks += 2)
-          mma_ss_mn2(tmem + col_o, vd + ks * 128, pd + ks * 128, id_o, !(first_u && ks == 0));
+        for (int ks = 2; ks < kUnit / 16; ks += 2)
+          mma_ss_mn2<0>(tmem + col_o, vd + ks * 128, pd + ks * 128, id_o, true);
         commit(&pv_empty[vb]);
         if (last_u) commit(o_full);
       };

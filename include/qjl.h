@@ -445,8 +445,12 @@ size_t qjl_tree_attention_workspace_bytes(const qjl_ctx* ctx, int B, int N, int 
  *   Precision: fp32 queries take fp32 products throughout. bf16 queries take the
  *      tensor cores: the projected query in fp16 (scaled by a power of two per
  *      row, its largest entry in [2^14, 2^15)), softmax weights and dequantised
- *      values in fp16 (at most 2^-11 relative each, an eighth of the output's
- *      own bf16 rounding), all sums in fp32.
+ *      values in fp16, all sums in fp32. Weights and values are held to 2^-11 of
+ *      themselves (an eighth of the output's own bf16 rounding), but for
+ *      - weights below 2^-18 of the row's largest: to 2^-29 of it, so that n such
+ *        tokens move an output by n 2^-29 max |V_hat| at most;
+ *      - values of a (sequence, kv head) where a group's finite |scale| is 2^11 or
+ *        its finite |zero| 2^15 and more: to 2^-11 of themselves or 2^-20.
  *   workspace: device, qjl_tree_attention_workspace_bytes bytes, 16-byte
  *      aligned, no initial contents needed. Calls that share one must not
  *      overlap on the GPU.
