@@ -91,6 +91,15 @@ qjl_status check_device(const qjl_ctx* ctx, const char* fn) {
   return QJL_OK;
 }
 
+// A draft cache is read with the committed cache's heads and outlier channels.
+qjl_status check_draft(const qjl_ctx* ctx, const qjl_cache* cache, const qjl_cache* draft, const char* fn) {
+  if (draft->B != cache->B || draft->Hkv != cache->Hkv)
+    return fail(QJL_ERR_ARG, std::string(fn) + ": the draft cache must have the cache's B and Hkv");
+  if (ctx->n_out > 0 && draft->outlier_idx != cache->outlier_idx)
+    return fail(QJL_ERR_ARG, std::string(fn) + ": the draft cache must share the cache's outlier_idx");
+  return QJL_OK;
+}
+
 // The context's wait limit in cycles at the maximum SM clock (a lower clock
 // only makes the wait longer in time).
 unsigned long long wait_cycles(const qjl_ctx* ctx) {
@@ -702,9 +711,8 @@ qjl_status qjl_tree_attention(qjl_ctx* ctx, const qjl_cache* cache, const qjl_ca
   qjl_status st = check_cache(ctx, cache);
   if (st == QJL_OK) st = check_cache(ctx, draft);
   if (st == QJL_OK) st = check_device(ctx, "qjl_tree_attention");
+  if (st == QJL_OK) st = check_draft(ctx, cache, draft, "qjl_tree_attention");
   if (st != QJL_OK) return st;
-  if (draft->B != cache->B || draft->Hkv != cache->Hkv)
-    return fail(QJL_ERR_ARG, "qjl_tree_attention: the draft cache must have the cache's B and Hkv");
   if (N < 1 || N > qjl::kMaxDrafts || N > draft->cap)
     return fail(QJL_ERR_ARG, "qjl_tree_attention: N must be in [1, 64] and at most the draft cache's cap");
   if (dtype != QJL_BF16 && dtype != QJL_FP32) return fail(QJL_ERR_ARG, "dtype must be QJL_BF16 or QJL_FP32");
@@ -766,9 +774,8 @@ qjl_status qjl_cache_commit(qjl_ctx* ctx, const qjl_cache* cache, const qjl_cach
   qjl_status st = check_cache(ctx, cache);
   if (st == QJL_OK) st = check_cache(ctx, draft);
   if (st == QJL_OK) st = check_device(ctx, "qjl_cache_commit");
+  if (st == QJL_OK) st = check_draft(ctx, cache, draft, "qjl_cache_commit");
   if (st != QJL_OK) return st;
-  if (draft->B != cache->B || draft->Hkv != cache->Hkv)
-    return fail(QJL_ERR_ARG, "qjl_cache_commit: the draft cache must have the cache's B and Hkv");
   if (draft->tiles == cache->tiles) return fail(QJL_ERR_ARG, "qjl_cache_commit: the two caches share their tiles");
   if (A < 0 || A > 65535 * 8) return fail(QJL_ERR_ARG, "qjl_cache_commit: A must be in [0, 524280]");
   if ((A > 0 && !path) || !n_accepted || !seqlens)

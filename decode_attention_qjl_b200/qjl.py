@@ -481,6 +481,12 @@ def _head_rows(fn: str, name: str, t, shape, dtype):
     return st
 
 
+def _check_draft(fn: str, cache, draft):
+    """The two caches must be of one context: the library reads the draft's tiles with the context's layout."""
+    if (draft.m, draft.m_out, draft.value_bits) != (cache.m, cache.m_out, cache.value_bits):
+        raise ValueError(f"{fn}: the draft cache has another layout than the cache (see QJLCache.draft)")
+
+
 def qjl_rope_init(rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0,
                   original_len: float = 0.0, low: float = 1.0, high: float = 4.0,
                   amplitude: float = 1.0) -> qjl_rope_table:
@@ -563,6 +569,7 @@ def qjl_tree_attention(ctx, cache: QJLCache, draft: QJLCache, Q, T: int, O, seql
     import torch
 
     fn = "qjl_tree_attention"
+    _check_draft(fn, cache, draft)
     shape = Q.shape
     if len(shape) != 4 or shape[0] != cache.B or shape[3] != HEAD_DIM:
         raise ValueError(f"qjl_tree_attention: Q must be [{cache.B}, N, Hq, {HEAD_DIM}]")
@@ -590,6 +597,7 @@ def qjl_cache_commit(ctx, cache: QJLCache, draft: QJLCache, path, n_accepted, se
     import torch
 
     fn = "qjl_cache_commit"
+    _check_draft(fn, cache, draft)
     A, rows = path.shape[-1], (cache.B,)
     ptrs = [_index_ptr(fn, "path", path, (cache.B, A), torch.int32)]
     for name, t in (("n_accepted", n_accepted), ("seqlens", seqlens), ("seqlens_out", seqlens_out)):

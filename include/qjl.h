@@ -334,10 +334,11 @@ qjl_status qjl_decode_workspace_status(const qjl_ctx* ctx, void* workspace, int 
  * dense keys and values. The pages have no counterpart: they describe decoding
  * one token at a time.
  *
- * A draft cache is a qjl_cache of the same context, B and Hkv whose
- * outlier_idx is the committed cache's, so that its keys are sketched with the
- * channels chosen at prefill; slot i of (b, kv head) holds drafted token i of
- * sequence b. cap = 64 is enough (at most 64 drafts).
+ * A draft cache is a qjl_cache of the same context, B and Hkv that shares the
+ * committed cache's outlier_idx array (another one is QJL_ERR_ARG when the
+ * context has outliers), so that its keys are sketched with the channels chosen
+ * at prefill; slot i of (b, kv head) holds drafted token i of sequence b.
+ * cap = 64 is enough (at most 64 drafts).
  *
  * These entry points run on the device of the context, which must be the
  * current one (else QJL_ERR_ARG); qjl_rope runs on the current device.

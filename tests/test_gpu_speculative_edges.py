@@ -148,3 +148,27 @@ def test_tree_small_groups_beside_groups_past_the_fp16_range():
                 err = np.abs(got[0, i, 2 * hk + g] - v[i])
                 assert np.all(err <= tol), (i, float((err - tol).max()))
             assert not np.any(np.isinf(got[0, i]))
+
+
+# ------------------------------------------------------------------ draft caches
+
+def test_draft_cache_with_other_outlier_channels_is_refused():
+    case = Case(2, 2, 4, 100, 4)
+    other = case.ctx.allocate_cache(2, 2, 64)  # channels of its own
+    out, lens = torch.full_like(case.Q, 3.0), torch.tensor([100, 50], dtype=torch.int32, device="cuda")
+    ws = case.ctx.tree_workspace(2, 4, 8, 2)
+    with pytest.raises(Q.QJLError, match="outlier_idx"):
+        Q.qjl_tree_attention(case.ctx.handle, case.cache, other, case.Q, 100, out, workspace=ws)
+    before = case.cache.tiles.clone()
+    with pytest.raises(Q.QJLError, match="outlier_idx"):
+        Q.qjl_cache_commit(case.ctx.handle, case.cache, other, torch.zeros(2, 1, dtype=torch.int32, device="cuda"),
+                           torch.ones_like(lens), lens)
+    torch.cuda.synchronize()
+    assert torch.all(out == 3.0) and torch.equal(case.cache.tiles, before)  # nothing was launched
+    # without outliers the arrays hold nothing and may differ
+    case = Case(1, 2, 4, 100, 4, m_out=0, n_outlier=0)
+    other = case.ctx.allocate_cache(1, 2, 64)
+    other.tiles.copy_(case.draft.tiles)
+    want = case.tree()
+    case.draft = other
+    assert torch.equal(case.tree(), want)
