@@ -44,6 +44,11 @@ qjl_status cuda_fail(cudaError_t e, const char* where) {
   return fail(QJL_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 qjl_status check_dims(int d, int m, int m_out, int n_outlier) {
@@ -771,20 +776,27 @@ qjl_status qjl_tree_attention(qjl_ctx* ctx, const qjl_cache* cache, const qjl_ca
 
 qjl_status qjl_cache_commit(qjl_ctx* ctx, const qjl_cache* cache, const qjl_cache* draft, int A, const int32_t* path,
                             const int32_t* n_accepted, const int32_t* seqlens, int32_t* seqlens_out, void* stream) {
+  if (A < 0 || A > 65535 * 8) return fail(QJL_ERR_ARG, "qjl_cache_commit: A must be in [0, 524280]");
+  if ((A > 0 && !path) || !n_accepted || !seqlens)
+    return fail(QJL_ERR_ARG, "qjl_cache_commit: null path, n_accepted or seqlens");
+  if (cache && cache->B > 0 && seqlens_out) {  // blocks read the inputs while another one writes it
+    const size_t row = static_cast<size_t>(cache->B) * sizeof(int32_t);
+    if (overlap(seqlens_out, row, seqlens, row)) return fail(QJL_ERR_ARG, "qjl_cache_commit: seqlens_out overlaps seqlens");
+    if (overlap(seqlens_out, row, n_accepted, row))
+      return fail(QJL_ERR_ARG, "qjl_cache_commit: seqlens_out overlaps n_accepted");
+    if (A > 0 && overlap(seqlens_out, row, path, row * A))
+      return fail(QJL_ERR_ARG, "qjl_cache_commit: seqlens_out overlaps path");
+  }
   qjl_status st = check_cache(ctx, cache);
   if (st == QJL_OK) st = check_cache(ctx, draft);
   if (st == QJL_OK) st = check_device(ctx, "qjl_cache_commit");
   if (st == QJL_OK) st = check_draft(ctx, cache, draft, "qjl_cache_commit");
   if (st != QJL_OK) return st;
-  if (draft->tiles == cache->tiles) return fail(QJL_ERR_ARG, "qjl_cache_commit: the two caches share their tiles");
-  if (A < 0 || A > 65535 * 8) return fail(QJL_ERR_ARG, "qjl_cache_commit: A must be in [0, 524280]");
-  if ((A > 0 && !path) || !n_accepted || !seqlens)
-    return fail(QJL_ERR_ARG, "qjl_cache_commit: null path, n_accepted or seqlens");
-  if (seqlens_out) {
-    const int32_t *a = seqlens, *o = seqlens_out;
-    if (a < o + cache->B && o < a + cache->B)
-      return fail(QJL_ERR_ARG, "qjl_cache_commit: seqlens_out overlaps seqlens");
-  }
+  const size_t tile = qjl::tile_layout(ctx->m, ctx->m_out, ctx->vbits).bytes;
+  const size_t rows = static_cast<size_t>(cache->B) * cache->Hkv;
+  if (overlap(cache->tiles, rows * (cache->cap / qjl::kDecodeTileTokens) * tile, draft->tiles,
+              rows * (draft->cap / qjl::kDecodeTileTokens) * tile))
+    return fail(QJL_ERR_ARG, "qjl_cache_commit: the two caches share tiles");
   if (cache->B > 65535) return fail(QJL_ERR_UNSUPPORTED, "B must be at most 65535");
   qjl::CommitParams p{};
   p.tiles = static_cast<unsigned char*>(cache->tiles);

@@ -593,7 +593,7 @@ def qjl_tree_attention(ctx, cache: QJLCache, draft: QJLCache, Q, T: int, O, seql
 
 def qjl_cache_commit(ctx, cache: QJLCache, draft: QJLCache, path, n_accepted, seqlens, seqlens_out=None, stream=None):
     """Copy draft slots path[b, j], j < n_accepted[b], to cache slots seqlens[b] + j; path: device int32 [B, A],
-    the others int32 [B]. seqlens_out (not seqlens itself) receives the new lengths."""
+    the others int32 [B]. seqlens_out (none of the inputs) receives the new lengths."""
     import torch
 
     fn = "qjl_cache_commit"

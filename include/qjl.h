@@ -473,8 +473,8 @@ qjl_status qjl_tree_attention(qjl_ctx* ctx, const qjl_cache* cache, const qjl_ca
  *   the draft cache or a target slot >= cap is skipped. seqlens_out[b] =
  *   min(len_b + n_accepted[b], cap).
  *   path: device int32 [B, A]; n_accepted, seqlens, seqlens_out: device int32
- *   [B]; seqlens_out must not overlap seqlens, and may be NULL. The two caches
- *   must not share tiles.
+ *   [B]; seqlens_out must not overlap seqlens, n_accepted or path, and may be
+ *   NULL. The two caches must not share tiles, not in part either.
  *   Errors: QJL_ERR_ARG, QJL_ERR_CUDA. A == 0 only writes seqlens_out.
  */
 qjl_status qjl_cache_commit(qjl_ctx* ctx, const qjl_cache* cache, const qjl_cache* draft, int A, const int32_t* path,

@@ -172,3 +172,29 @@ def test_draft_cache_with_other_outlier_channels_is_refused():
     want = case.tree()
     case.draft = other
     assert torch.equal(case.tree(), want)
+
+
+# ------------------------------------------------------------------ commit
+
+def test_commit_between_overlapping_slabs_is_refused():
+    """A draft slab that begins inside the cache's: source and target rows would be the same bytes."""
+    case = Case(2, 2, 1, 128, 4)  # two tiles a slab
+    flat = case.cache.tiles.flatten(0, 2)
+    lens = torch.tensor([100, 50], dtype=torch.int32, device="cuda")
+    path = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    before = case.cache.tiles.clone()
+    for first in (0, 1, 4):
+        part = Q.QJLCache(case.cache.outlier_idx, flat[first:first + 4].view(2, 2, 1, -1), 2, 2, 64, case.m, case.m_out)
+        with pytest.raises(Q.QJLError, match="share"):
+            Q.qjl_cache_commit(case.ctx.handle, case.cache, part, path, torch.ones_like(lens), lens)
+    torch.cuda.synchronize()
+    assert torch.equal(case.cache.tiles, before)
+    # side by side in one buffer they may lie
+    buf = torch.zeros(12, flat.shape[-1], dtype=torch.uint8, device="cuda")
+    buf[:8].copy_(flat)
+    buf[8:].copy_(case.draft.tiles.flatten(0, 2))
+    make = lambda t, n: Q.QJLCache(case.cache.outlier_idx, t, 2, 2, 64 * n, case.m, case.m_out)  # noqa: E731
+    Q.qjl_cache_commit(case.ctx.handle, make(buf[:8].view(2, 2, 2, -1), 2), make(buf[8:].view(2, 2, 1, -1), 1), path,
+                       torch.ones_like(lens), lens)
+    Q.qjl_cache_commit(case.ctx.handle, case.cache, case.draft, path, torch.ones_like(lens), lens)
+    assert torch.equal(buf[:8], flat) and not torch.equal(case.cache.tiles, before)
