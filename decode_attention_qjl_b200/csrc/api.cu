@@ -734,7 +734,7 @@ qjl_status qjl_tree_attention(qjl_ctx* ctx, const qjl_cache* cache, const qjl_ca
   if (tree_mask && (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
     return fail(QJL_ERR_ARG, "qjl_tree_attention: tree_mask must be 8-byte aligned");
   if (!workspace || !aligned16(workspace) ||
-      workspace_bytes < qjl_tree_attention_workspace_bytes(ctx, cache->B, N, Hq, cache->Hkv))
+      workspace_bytes < qjl::tree_ws_used(cache->B, N, Hq, cache->Hkv, ctx->m, ctx->m_out, ctx->vbits, ctx->num_sms))
     return fail(QJL_ERR_WORKSPACE, "qjl_tree_attention: workspace missing, misaligned or too small");
   qjl::TreeParams p{};
   p.tiles = static_cast<const unsigned char*>(cache->tiles);

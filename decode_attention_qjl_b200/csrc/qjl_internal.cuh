@@ -355,6 +355,7 @@ void tc_fill_s_image(const uint16_t* S, int rows, uint16_t* img);  // host: [row
 cudaError_t launch_rope(const RopeParams& p, qjl_dtype dt, cudaStream_t s);
 cudaError_t launch_cache_read(const ReadParams& p, qjl_dtype dt, cudaStream_t s);
 cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t s);
+size_t tree_ws_used(int B, int N, int Hq, int Hkv, int m, int m_out, int vbits, int num_sms);
 size_t tree_ws_bytes(int B, int N, int Hq, int Hkv, int m, int m_out, int vbits, int num_sms);
 size_t tree_tc_ws_bytes(int B, int N, int Hq, int Hkv, int m, int m_out, int vbits, int num_sms);
 cudaError_t launch_tree_attention_tc(const TreeParams& p, cudaStream_t s);

@@ -423,7 +423,8 @@ qjl_status qjl_cache_read(qjl_ctx* ctx, const qjl_cache* cache, int T, const int
 
 /*
  * qjl_tree_attention_workspace_bytes - device workspace of qjl_tree_attention
- * for B sequences of up to N drafted tokens; 0 for an invalid shape.
+ * for B sequences of up to N drafted tokens; 0 for an invalid shape. It never
+ * falls as N grows, and serves calls of any smaller N too.
  */
 size_t qjl_tree_attention_workspace_bytes(const qjl_ctx* ctx, int B, int N, int Hq, int Hkv);
 
@@ -452,9 +453,9 @@ size_t qjl_tree_attention_workspace_bytes(const qjl_ctx* ctx, int B, int N, int 
  *        tokens move an output by n 2^-29 max |V_hat| at most;
  *      - values of a (sequence, kv head) where a group's finite |scale| is 2^11 or
  *        its finite |zero| 2^15 and more: to 2^-11 of themselves or 2^-20.
- *   workspace: device, qjl_tree_attention_workspace_bytes bytes, 16-byte
- *      aligned, no initial contents needed. Calls that share one must not
- *      overlap on the GPU.
+ *   workspace: device, qjl_tree_attention_workspace_bytes bytes for this N or a
+ *      larger one, 16-byte aligned, no initial contents needed. Calls that share
+ *      one must not overlap on the GPU.
  *   Every wait inside is bounded by qjl_set_wait_limit; when one runs out, the
  *   rows it belongs to become NaN.
  *   Errors: QJL_ERR_ARG, QJL_ERR_UNSUPPORTED (Hq / Hkv not 1, 2, 4 or 8),

@@ -174,6 +174,30 @@ def test_draft_cache_with_other_outlier_channels_is_refused():
     assert torch.equal(case.tree(), want)
 
 
+# ------------------------------------------------------------------ workspaces
+
+@pytest.mark.parametrize("shape", [(1, 32, 8), (1, 64, 8), (2, 8, 8), (16, 32, 8), (1, 8, 1), (3, 2, 1)])
+@pytest.mark.parametrize("kw", [{}, {"m": 512, "m_out": 256, "value_bits": 2}, {"m": 96, "m_out": 0, "n_outlier": 0}])
+def test_tree_workspace_never_falls_as_drafts_grow(shape, kw):
+    B, Hq, Hkv = shape
+    ctx = Q.QJLContext(0, D, **kw)
+    sizes = [Q.qjl_tree_attention_workspace_bytes(ctx.handle, B, n, Hq, Hkv) for n in range(1, 65)]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+    ctx.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tree_smaller_steps_in_the_workspace_of_a_larger_one(dtype):
+    """33 drafts of 4 query heads make two row blocks, 32 one larger one."""
+    case = Case(1, 2, 4, 200, 33, dtype)
+    ws = case.ctx.tree_workspace(1, 33, 8, 2)
+    for n in (33, 32, 31, 16, 1):
+        mask = random_tree(1, n, n)
+        own = case.ctx.tree_workspace(1, n, 8, 2)
+        q, case.N = case.Q[:, :n].contiguous(), n
+        assert torch.equal(case.tree(mask, Q_=q, ws=ws), case.tree(mask, Q_=q, ws=own)), n
+
+
 # ------------------------------------------------------------------ commit
 
 def test_commit_between_overlapping_slabs_is_refused():
