@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const __grid_cons
     const int64_t bt = tok0 + k;
     if (bt >= tokens) break;
     const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt - static_cast<int64_t>(b) * p.T);
-    const int pos = p.positions ? p.positions[bt] : (p.t_start ? p.t_start[b] : 0) + t;
+    const int64_t pos = p.positions ? p.positions[bt] : static_cast<int64_t>(p.t_start ? p.t_start[b] : 0) + t;
     const double x = static_cast<double>(pos) * p.table.turns[i];
     float sn, cs;
     sincospif(static_cast<float>(2.0 * (x - rint(x))), &sn, &cs);  // half turns in [-1, 1]

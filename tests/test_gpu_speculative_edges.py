@@ -198,6 +198,31 @@ def test_tree_smaller_steps_in_the_workspace_of_a_larger_one(dtype):
         assert torch.equal(case.tree(mask, Q_=q, ws=ws), case.tree(mask, Q_=q, ws=own)), n
 
 
+# ------------------------------------------------------------------ rotary positions
+
+def check_rope_far(got, x, pos, inverse=False):
+    """The plain rotation of all 128 dims against the formula with 64-bit mantissas, fp32 data. 12 u of the magnitudes
+    as in test_gpu_speculative; the angle: the table's entry and its product with the position round by 2^-53 each and
+    the table's own power and quotient by as much together, 2^-51 |P f| covers them."""
+    x64, got = C.to64(x).astype(np.longdouble), C.to64(got)
+    for i in range(D // 2):
+        f = np.longdouble(10000.0) ** (-np.longdouble(2 * i) / D)
+        a = pos.astype(np.longdouble) * f * (-1 if inverse else 1)
+        c, s = np.cos(a)[:, None, :], np.sin(a)[:, None, :]
+        u, v = x64[..., i], x64[..., i + D // 2]
+        tol = (np.abs(u) + np.abs(v)) * (13 * U + 2.0 ** -51 * np.abs(a)[:, None, :])
+        assert np.all(np.abs(got[..., i] - (u * c - v * s)) <= tol), i
+        assert np.all(np.abs(got[..., i + D // 2] - (v * c + u * s)) <= tol), i
+
+
+def test_rope_start_positions_run_past_31_bits():
+    """P = t_start + t is not bound to int32."""
+    start = np.array([2 ** 31 - 5, -2 ** 31, 2 ** 31 - 1], np.int64)
+    x = torch.randn(3, 2, 9, D, generator=torch.Generator().manual_seed(3))
+    got = Q.qjl_rope(Q.qjl_rope_init(), x.cuda(), t_start=torch.from_numpy(start.astype(np.int32)).cuda())
+    check_rope_far(got, x, start[:, None] + np.arange(9))
+
+
 # ------------------------------------------------------------------ commit
 
 def test_commit_between_overlapping_slabs_is_refused():
