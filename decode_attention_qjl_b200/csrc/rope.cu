@@ -1,10 +1,12 @@
 // Rotary positions of a step's queries and keys.
 //
 // Plane i of a head turns by a = P f_i: (u, v) -> (u cos a - v sin a,
-// v cos a + u sin a). The angle is reduced in fp64: P f_i / (2 pi) minus its
-// nearest integer is exact to 2^-22 of a turn's fp32 resolution for every
-// int32 position, where an fp32 product would be off by whole radians near a
-// million; sin and cos are then taken in fp32 of the reduced turn.
+// v cos a + u sin a). The angle is reduced in fp64, P f_i / (2 pi) minus its
+// nearest integer: the table's entry and the product round by 2^-53 each, which
+// leaves the angle within 2^-51 |P f_i| radians (the entry's own quotient and
+// power included), below fp32's resolution of a radian up to |P| = 2^27 and 1e-6
+// at 2^31, where an fp32 product would be off by whole radians near a million; sin
+// and cos are then taken in fp32 of the reduced turn.
 //
 // Bound: HBM, every element is read and written once. A block takes TT tokens
 // and all their heads: its threads compute the tokens' sines once into shared

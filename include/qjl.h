@@ -392,8 +392,9 @@ qjl_status qjl_rope_init(int rot_dim, double base, qjl_rope_layout layout, doubl
  *     y_u = amplitude (x_u cos a - x_v sin a),
  *     y_v = amplitude (x_v cos a + x_u sin a);   inverse != 0: a -> -a,
  *   which is the gradient with respect to x of the forward rotation, and with
- *   amplitude 1 its inverse. Angles are reduced in fp64, so far positions lose
- *   nothing; sin, cos and the products are fp32, rounded once to the dtype.
+ *   amplitude 1 its inverse. Angles are reduced in fp64, to 2^-51 |P f_i|
+ *   radians (below fp32's own rounding up to |P| = 2^27, 1e-6 at 2^31); sin, cos
+ *   and the products are fp32, rounded once to the dtype.
  *   heads: n_heads (1 or 2) tensors [B, H, T, d] (d = 128) of the same dtype,
  *   16-byte aligned.
  *   positions: device int32 [B, T], or NULL: P = (t_start ? t_start[b] : 0) + t.

@@ -223,6 +223,16 @@ def test_rope_start_positions_run_past_31_bits():
     check_rope_far(got, x, start[:, None] + np.arange(9))
 
 
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_at_the_ends_of_the_position_range(inverse):
+    g = torch.Generator().manual_seed(4)
+    near = torch.randint(0, 2000, (4, 50), generator=g)
+    ends = torch.tensor([2 ** 31 - 2001, -2 ** 31, 2 ** 27, -2 ** 24])[:, None] + near
+    x = torch.randn(4, 2, 50, D, generator=g)
+    got = Q.qjl_rope(Q.qjl_rope_init(), x.cuda(), positions=ends.to(torch.int32).cuda(), inverse=inverse)
+    check_rope_far(got, x, ends.numpy(), inverse)
+
+
 # ------------------------------------------------------------------ commit
 
 def test_commit_between_overlapping_slabs_is_refused():
