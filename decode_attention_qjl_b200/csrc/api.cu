@@ -759,7 +759,6 @@ qjl_status qjl_tree_attention(qjl_ctx* ctx, const qjl_cache* cache, const qjl_ca
   p.n_draft = n_draft;
   p.mask = tree_mask;
   p.S = ctx->S;
-  p.St = ctx->St;
   p.S_out = ctx->S_out;
   p.S_frag = reinterpret_cast<const uint4*>(ctx->S_frag);
   p.idx = cache->outlier_idx;

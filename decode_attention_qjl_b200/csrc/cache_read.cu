@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kReadThreads, 1) cache_read_kernel(const __gri
   } else if (warp < 16) {
     // ============================================================ values
     const int tt = 32 * (warp & 3) + lane, part = (warp - 8) >> 2;  // dims 64 part ..
-RowStage<T, SEG> out{stage + 32 * SEG * (warp - 8), 0u, nullptr, p.v_st};
+    RowStage<T, SEG> out{stage + 32 * SEG * (warp - 8), 0u, nullptr, p.v_st};
     struct Codes {  // of this thread's half token, fetched one unit ahead of their use
       uint2 sz;
       uint4 cw[2];

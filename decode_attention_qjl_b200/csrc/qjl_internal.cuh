@@ -322,7 +322,7 @@ struct TreeParams {
   int64_t q_sb, q_sn, q_sh;
   const int32_t *seqlens, *n_draft;
   const uint64_t* mask;
-  const __nv_bfloat16 *S, *St, *S_out;
+  const __nv_bfloat16 *S, *S_out;
   const uint4* S_frag;
   const int32_t* idx;
   float sm_scale_log2;
