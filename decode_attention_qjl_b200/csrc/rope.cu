@@ -15,14 +15,21 @@
 // u and u + rot/(2 e) in the half layout, u and u + d/(2 e) in the interleaved
 // one, e elements per chunk), and walks over the heads; eight (bf16) lanes cover
 // 128 consecutive bytes with every load and store. Measured, 32768 tokens of 64
-// heads, bf16: 188 us, 5.7 TB/s (six blocks per SM; 206 us with the five that 48
-// registers allow).
+// heads, bf16, two sets of buffers in turn: 190 us, 5.7 TB/s (half layout, 128
+// dims); 168 us, 6.4 TB/s (interleaved, 64 dims).
 #include "qjl_internal.cuh"
 
 namespace qjl {
 namespace {
 
 constexpr int kRopeThreads = 256;
+// Blocks that an SM holds, which sets the registers of a thread: as many as leave
+// at most 24 bytes of spills. bf16 in the half layout keeps the sines of 8 planes
+// and two chunks of 8 values. Measured with 6, 5, 4 and 3 blocks, 32768 tokens of
+// 64 heads: bf16 half 248, 207, 190, 210 us (half the dims 289, 208, 187, 206);
+// bf16 interleaved, 64 dims 184, 168, 177 us; fp32 half, 16384 tokens 174, 168, 171.
+template <typename T, int LAYOUT>
+constexpr int kRopeBlocks = sizeof(T) == 2 && LAYOUT == QJL_ROPE_HALF ? 4 : 5;
 
 template <typename T>
 struct Chunk;  // 16 bytes as fp32 values
@@ -61,7 +68,7 @@ struct Chunk<float> {
 };
 
 template <typename T, int LAYOUT, int TT>
-__global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, (kRopeBlocks<T, LAYOUT>)) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int E = Chunk<T>::n;              // elements of a chunk
   constexpr int kPairs = kHeadDim / (2 * E);  // chunk pairs of a row
   __shared__ float2 turn[TT][kHeadDim / 2];   // (cos, sin) of plane i of token k, the amplitude in both
