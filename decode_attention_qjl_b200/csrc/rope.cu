@@ -153,22 +153,32 @@ __global__ void __launch_bounds__(kRopeThreads, (kRopeBlocks<T, LAYOUT>)) rope_k
   }
 }
 
-template <typename T, int TT>
+template <typename T, int LAYOUT, int TT>
 cudaError_t launch(const RopeParams& p, cudaStream_t s) {
   const int64_t blocks = (static_cast<int64_t>(p.B) * p.T + TT - 1) / TT;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const unsigned n = static_cast<unsigned>(blocks);
-  if (p.table.layout == QJL_ROPE_HALF)
-    rope_kernel<T, QJL_ROPE_HALF, TT><<<n, kRopeThreads, 0, s>>>(p);
-  else
-    rope_kernel<T, QJL_ROPE_INTERLEAVED, TT><<<n, kRopeThreads, 0, s>>>(p);
+  rope_kernel<T, LAYOUT, TT><<<static_cast<unsigned>(blocks), kRopeThreads, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+// A block per token while the device holds all of them at once, for the SMs'
+// sake; past that four tokens a block, which fill it with whole planes of sines.
+// Measured with 1 and 4 tokens a block (us), half layout, 40 heads: 592 tokens 5.5
+// and 7.2, 740 7.9 and 8.4, 1184 9.6 and 9.5, 2368 16.2 and 13.1; 10 heads: 444
+// 3.4 and 3.3, 1184 5.8 and 4.2.
+template <typename T, int LAYOUT>
+cudaError_t launch_l(const RopeParams& p, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  return static_cast<int64_t>(p.B) * p.T <= static_cast<int64_t>(kRopeBlocks<T, LAYOUT>) * sms ? launch<T, LAYOUT, 1>(p, s)
+                                                                                            : launch<T, LAYOUT, 4>(p, s);
 }
 
 template <typename T>
 cudaError_t launch_t(const RopeParams& p, cudaStream_t s) {
-  // four tokens a block fill it with whole planes of work; few tokens take a block each, for the SMs' sake
-  return static_cast<int64_t>(p.B) * p.T >= 4 * 148 ? launch<T, 4>(p, s) : launch<T, 1>(p, s);
+  return p.table.layout == QJL_ROPE_HALF ? launch_l<T, QJL_ROPE_HALF>(p, s) : launch_l<T, QJL_ROPE_INTERLEAVED>(p, s);
 }
 
 }  // namespace
