@@ -483,7 +483,7 @@ def _head_rows(fn: str, name: str, t, shape, dtype):
 
 def _check_draft(fn: str, cache, draft):
     """The two caches must be of one context: the library reads the draft's tiles with the context's layout."""
-    if (draft.m, draft.m_out, draft.value_bits) != (cache.m, cache.m_out, cache.value_bits):
+    if draft.m != cache.m or draft.m_out != cache.m_out or draft.value_bits != cache.value_bits:
         raise ValueError(f"{fn}: the draft cache has another layout than the cache (see QJLCache.draft)")
 
 
