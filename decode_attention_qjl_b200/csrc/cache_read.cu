@@ -21,9 +21,10 @@
 // per lane; 32 rows written by 32 lanes, a sector each, took 3.8 SM cycles per
 // sector (208 us for 1 M token-heads, bf16), so they turn a piece of their rows
 // through shared memory and write 128 bytes of a row with eight lanes.
-// Measured, 1 M token-heads, m = 256, bf16: 166 us, 4.0 TB/s (HBM's rate would
-// take 102); the roles' 13900 warp instructions per unit use two thirds of the
-// issue slots. Values alone take 80 us.
+// Measured, 1 M token-heads, m = 256, bf16: 186 us, 3.6 TB/s, on inputs that change
+// from call to call, 167 us in a row on unchanged ones (HBM's rate would take 102);
+// the roles' 13900 warp instructions per unit use two thirds of the issue slots.
+// Values alone take 80 us.
 #include "tc_common.cuh"
 
 namespace qjl {

@@ -32,7 +32,9 @@ constexpr int kTreeHalf = kTreeRows / 2;
 constexpr int kTreeProjSplit = 8; // blocks that share the projections of 8 rows
 
 int tree_row_blocks(int N, int G) { return (N * G + kTreeRows - 1) / kTreeRows; }
-// Splits of a pair's units: enough blocks for four per SM.
+// Splits of a pair's units: enough blocks for four per SM. With 1, 2, 4 and 8: 2 x
+// 4096 tokens, 56 rows on one kv head 90, 90, 68, 68 us; 8 x 4096, 64 rows, 4 kv heads
+// 855, 810, 781, 714; 2 x 1024 30 throughout. The workspace grows with them.
 int tree_splits(int pairs, int row_blocks, int num_sms) {
   const int64_t b = static_cast<int64_t>(pairs) * row_blocks;
   const int64_t n = (4 * static_cast<int64_t>(num_sms) + b - 1) / b;

@@ -34,16 +34,18 @@
 // the values of an item are kept as V_hat / 16, which no fp16 scale and zero push
 // past the range, to 2^-11 or 2^-20 absolute; that unit's product divides the
 // outputs so far by 16. (Dividing from the start lost the bits of small values;
-// looking for wide tokens costs 1 to 2 % of the long cases.) All sums are fp32.
+// looking for wide tokens costs 2 % of a long call with 64 rows, 8 % with 16.) All
+// sums are fp32.
 //
 // Bound: HBM below about 35 rows of a kv head (124 bytes against 896 flops per
 // row and token), the tensor rate above. Measured, 4 x 131072 tokens, 8 kv heads,
-// 64 rows: 357 us, where the tensor rate allows 146 and HBM 80; a unit costs
+// 64 rows: 360 us in a row on unchanged inputs, 388 on inputs that change from call
+// to call, where the tensor rate allows 146 and HBM 80; a unit costs
 // about 2600 SM cycles, its products 1060 (an mma of 128 x 64 x 16 takes 33), and
-// the roles issue 7200 warp instructions together, more than half of the slots:
-// 320 of a sign warp's 430 per unit are the logic of the expansion, 240 of a
-// value warp's 400 the dequantisation. With 16 rows the call takes 279 us. A
-// call's start, first unit, outputs and join cost about 35 us.
+// the roles issue 7500 warp instructions together, 59 % of the slots (320 of a sign
+// warp's 430 per unit are the logic of the expansion, 240 of a value warp's 400
+// the dequantisation); the rest are waits between roles. With 16 rows the call
+// takes 305 us. A call's start, first unit, outputs and join cost about 35 us.
 #include "tc_common.cuh"
 
 namespace qjl {
@@ -77,7 +79,9 @@ constexpr int kBadRing = 4;  // items whose drafted values may be in flight at o
 constexpr int kMiscBytes = 3 * 128 * 4 + 4 * 128 * 4 + 2 * 128 * 8 + kBadRing * 64 * 4 + (kBadRing + 2) * 4 + 32 * 8 + 64;
 
 // Row block, buffers and stages: the largest row block (fewest passes over the
-// cache) that leaves two stages, then a second weight buffer, then stages.
+// cache) that leaves two stages, then a second weight buffer, then stages. With at
+// most 64, 96 and 128 rows a block: 1 x 32768 tokens, 8 kv heads, 128 rows 80, 80, 89
+// us; 96 rows 79, 74, 74; 512 rows 207, 219, 217; 4 x 8192, 132 rows 110, 107, 107.
 TreeTcCfg tree_tc_cfg(int N, int G, int m, int m_out, int tile_bytes) {
   TreeTcCfg c{};
   const int R = N * G, limit = 227 * 1024 - 1024;
