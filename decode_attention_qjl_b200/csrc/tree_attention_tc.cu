@@ -75,7 +75,7 @@ struct TreeTcCfg {
   int stage;   // bytes of a stage
   int smem;
 };
-constexpr int kBadRing = 4;  // items whose drafted values may be in flight at once (three)
+constexpr int kBadRing = 4;  // items that the value warps may have begun and the weight warps not ended (three), and one
 constexpr int kMiscBytes = 3 * 128 * 4 + 4 * 128 * 4 + 2 * 128 * 8 + kBadRing * 64 * 4 + (kBadRing + 2) * 4 + 32 * 8 + 64;
 
 // Row block, buffers and stages: the largest row block (fewest passes over the
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
     const uint32_t key = (tt & 7) << 4;
     for (bool more = any; more && ok; more = w.next<true>(p), ++item) {  // (ok ends for all four warps at once)
       bool wide = false;  // the item's values are divided by 16 from here on
-      if (tt == 0) wides[item % kBadRing] = 0;
+      if (tt == 0) wides[item % kBadRing] = 0;  // (read at the item's end)
       for (int u = w.u0; u < w.u1 && ok; ++u) {
         ok = bar_wait(&raw_full[st], sph, limit, err) && bar_wait(&pv_empty[vb], vph, limit, err);
         ok = __all_sync(0xffffffffu, ok);
@@ -599,12 +599,14 @@ __global__ void __launch_bounds__(kTreeTcThreads, 1) tree_tc_kernel(const __grid
         const bool live = tt < w.tokens(u), draft = w.draft(u);
         const uint4 sz = *reinterpret_cast<const uint4*>(tile + t.tl.vsz + 16 * j);
         const uint32_t* szg = reinterpret_cast<const uint32_t*>(tile + t.tl.vsz + 16 * j);
-        if (v_any(!ok | (live & wide_token(sz)))) {  // seldom: a wide token, or a wait that ran out
+        // The four warps must agree on the unit's factor, and leave together when a wait ran out in one: one barrier,
+        // and seldom a second that tells which of the two it was.
+        if (v_any(!ok | (live & wide_token(sz)))) {
           ok = !v_any(!ok);
           if (!ok) break;
           if (!wide && tt == 0) {
             wides[item % kBadRing] = 1;
-            if (u > w.u0) wides[kBadRing + vb] = n;
+            if (u > w.u0) wides[kBadRing + vb] = n;  // this unit's product divides what the item has so far
           }
           wide = true;
         }

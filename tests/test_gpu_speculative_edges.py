@@ -128,6 +128,22 @@ def test_tree_one_value_past_the_fp16_range(token):
     assert torch.equal(case.tree(mask), got)
 
 
+def test_tree_wait_limits_where_values_pass_the_fp16_range():
+    case = Case(2, 4, 4, 6000, 8)
+    for t in range(0, 6000, 333):
+        set_value_group(case, case.cache, t, 2, 60000.0, -30000.0)
+    mask = random_tree(2, 8, 7)
+    want = case.tree(mask)
+    try:
+        Q.qjl_set_wait_limit(case.ctx.handle, 1)
+        out = case.tree(mask)
+        torch.cuda.synchronize()
+        assert torch.isnan(out).any()
+    finally:
+        Q.qjl_set_wait_limit(case.ctx.handle, 2_000_000_000)
+    assert torch.equal(case.tree(mask), want) and bool(torch.isfinite(want).all())
+
+
 def test_tree_small_groups_beside_groups_past_the_fp16_range():
     """From the first unit with a scale of 2^11 or a zero of 2^15 and more on, a kv head's values are held divided by
     16: they are then off by the roundings of zero / 16 and of the sum, half an fp16 subnormal step each:
